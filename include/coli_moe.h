@@ -327,6 +327,120 @@ coli_status coli_moe_forward_noalloc(const coli_moe_layer *L, const float *x,
                                      int32_t *wait_status_out, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit products with one scale per token and one per output channel, and a
+ * router over softmax or sigmoid scores.  They extend the pages' layer: its
+ * int8 container (one scale per row) against activations with one scale per
+ * token instead of one per 32 values, so that a product's whole sum stays in
+ * integers.  Together they form a routed layer in 8 bits: coli_moe_route_scored,
+ * coli_moe_dispatch, coli_quant_act_token, coli_gemm_q8_grouped (gate and up),
+ * coli_swiglu_quant_token, coli_gemm_q8_grouped (down), coli_moe_combine; and
+ * coli_gemm_q8 is the dense layers' product.
+ *
+ * Every call takes its element type (coli_dtype) for activations and results;
+ * scales, weights of the sum and biases are fp32.  Row strides (ld) are in
+ * elements and at least the row's length; elements of a row are consecutive.
+ * Rows that start 16-byte aligned are read and written in 16-byte words,
+ * others element by element.  The calls need no workspace, keep nothing and
+ * may be captured into a graph.  Buffers must not overlap unless stated.
+ * ------------------------------------------------------------------------- */
+typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
+
+/* Per-token int8 activations.  x [T][n], row stride ldx -> q [T][n] int8
+ * (contiguous, 16-byte aligned) and s [T] fp32: s = max|x| / 127 (fp32
+ * division); q = clamp(round_half_even(x / s), -127, 127); s = 0 gives q = 0.
+ * A row holding a NaN or an infinity gets s = NaN and q = 0, so every product
+ * made from it is NaN.  n a positive multiple of 32, at most 131040;
+ * 0 <= T <= 2^20. */
+coli_status coli_quant_act_token(int32_t dtype, const void *x, int64_t ldx,
+                                 int32_t T, int32_t n, int8_t *q, float *s,
+                                 void *stream);
+
+/* The same of h = silu(g) * u (SwiGLU), silu(g) = g / (1 + exp(-g)), with h
+ * evaluated in fp64 and rounded once to fp32.  g, u [T][n] with row strides
+ * ldg, ldu (the halves of one [T][2n] buffer are u = g + n, ld = 2n).
+ * 0 <= T <= 2^25 (a row for each routed pair). */
+coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
+                                    const void *u, int64_t ldu, int32_t T,
+                                    int32_t n, int8_t *q, float *s,
+                                    void *stream);
+
+/* y [T][N] = s_t * ws_n * sum_k q[t][k] * w[n][k] (+ bias_n), row stride ldy.
+ * q [T][K] and s [T] as coli_quant_act_token gives them, w [N][K] and ws [N]
+ * an int8 container (coli_quant_pack with COLI_Q8), bias [N] or NULL.  The
+ * sum is exact; it is converted to fp32, multiplied by the product of the
+ * scales, the bias is added, and the result is rounded once to y's type (past
+ * the largest fp16 value: infinity).  K a positive multiple of 32, at most
+ * 131040; 0 <= T <= 2^20; N >= 1; q, w 16-byte aligned.  Sizes whose
+ * launch would not fit a grid return COLI_ERR_UNSUPPORTED. */
+coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T,
+                         const uint8_t *w, const float *ws, int32_t N,
+                         int32_t K, const float *bias, int32_t dtype, void *y,
+                         int64_t ldy, void *stream);
+
+/* The experts' form: for every position i in [offs[e], offs[e + 1]) of every
+ * expert e, with p = perm[i], y[p] = the product of row p / fan of q with
+ * expert e's weights w [E][N][K], ws [E][N].  offs [E + 1] and perm [P] are
+ * coli_moe_dispatch's (P = T * k).  fan = k reads one row per token (gate and
+ * up), fan = 1 one row per (token, slot) pair (down).  q holds `rows` rows,
+ * y P rows.  Rows of y that no position names are left as they are.  Positions
+ * past P, and pairs outside [0, P) or whose row of q is past `rows`, are
+ * skipped.  1 <= E <= 1024, 0 <= P <= 2^25, fan >= 1; the rest as for
+ * coli_gemm_q8. */
+coli_status coli_gemm_q8_grouped(const int8_t *q, const float *s, int32_t rows,
+                                 const uint8_t *w, const float *ws, int32_t E,
+                                 int32_t N, int32_t K, const int32_t *offs,
+                                 const int32_t *perm, int32_t P, int32_t fan,
+                                 int32_t dtype, void *y, int64_t ldy,
+                                 void *stream);
+
+/* y [T][H] = add[t] + sum_j w[t][j] * o[t * k + j], in slot order and fp32,
+ * rounded once.  o [T * k][H], w [T][k]; idx [T][k] or NULL: slots with a
+ * negative idx are not read.  add [T][H] (for example the shared expert's
+ * output) or NULL; it may be y itself.  1 <= k <= 32, 1 <= H <= 131072,
+ * 0 <= T <= 2^20. */
+coli_status coli_moe_combine(int32_t dtype, const void *o, int64_t ldo,
+                             const int32_t *idx, const float *w, int32_t T,
+                             int32_t k, int32_t H, const void *add,
+                             int64_t ldadd, void *y, int64_t ldy, void *stream);
+
+typedef enum { COLI_SCORE_SIGMOID = 0, COLI_SCORE_SOFTMAX = 1 } coli_score;
+typedef enum { COLI_GROUP_TOP2 = 0, COLI_GROUP_MAX = 1 } coli_group_score;
+
+/* Router over scores (host struct).  Limits as for coli_router_cfg. */
+typedef struct {
+  int32_t n_experts;           /* E */
+  int32_t top_k;               /* k */
+  int32_t n_group;             /* contiguous groups of E / n_group experts */
+  int32_t topk_group;          /* groups kept */
+  int32_t score;               /* coli_score */
+  int32_t group_score;         /* coli_group_score */
+  int32_t norm_topk_prob;      /* 1: selected weights normalised to sum 1 */
+  float routed_scaling_factor;
+} coli_score_cfg;
+
+/* Routing over softmax or sigmoid scores.  logits [T][E], row stride ld, in
+ * any coli_dtype; bias [E] fp32 or NULL.  An expert whose logit is NaN or -inf
+ * is off: it has no share in the softmax and is never chosen.  For each token:
+ *   p_e = softmax or sigmoid of the logits, evaluated in fp64 and rounded once
+ *   to fp32 (experts at +inf share a softmax equally); c_e = p_e + bias_e (a
+ *   sum of NaN or -inf: never chosen);
+ *   a group's score is its largest c, or the sum of its two largest
+ *   (COLI_GROUP_TOP2; the one if it has only one); the topk_group best groups
+ *   are kept (ties: lower index), when there are more;
+ *   the top_k largest c of their experts (ties: lower index) in rank order;
+ *   w_j = p_j / S * routed_scaling_factor, S the fp32 sum of the chosen p in
+ *   rank order (S = 0 gives weights 0); p_j * routed_scaling_factor when
+ *   norm_topk_prob is 0.  (Softmax with norm_topk_prob = 1 equals a softmax
+ *   over the chosen logits alone.)
+ * Slots past the experts that can be chosen get idx -1 and w 0.  Writes
+ * topk_idx [T][k] int32 and topk_w [T][k] fp32.  0 <= T <= 2^20. */
+coli_status coli_moe_route_scored(const coli_score_cfg *cfg, int32_t dtype,
+                                  const void *logits, int64_t ld,
+                                  const float *bias, int32_t T,
+                                  int32_t *topk_idx, float *topk_w,
+                                  void *stream);
+
+/* ---------------------------------------------------------------------------
  * Tiered expert residency.  The pages treat device memory, host memory and
  * disk as one hierarchy and stream the routed experts a token needs from the
  * slower tier (CSDN feature, "把内存、显存和磁盘当成同一块蛋糕"), behind a

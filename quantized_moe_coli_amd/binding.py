@@ -20,6 +20,9 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "coli_moe.h")
 
 COLI_OK, COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, COLI_ERR_WORKSPACE, COLI_ERR_DEVICE = range(5)
 COLI_Q8, COLI_Q4, COLI_Q2 = 8, 4, 2
+COLI_F32, COLI_BF16, COLI_F16 = range(3)
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GROUP_TOP2, GROUP_MAX = 0, 1
 
 
 class ColiError(RuntimeError):
@@ -65,6 +68,13 @@ class SpecGuardC(ctypes.Structure):
                 ("next_draft", ctypes.c_int32), ("since_probe", ctypes.c_int32),
                 ("steps", ctypes.c_int64), ("draft_steps", ctypes.c_int64),
                 ("tokens", ctypes.c_int64)]
+
+
+class ScoreCfg(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("norm_topk_prob", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float)]
 
 
 class CacheLayoutC(ctypes.Structure):
@@ -137,6 +147,17 @@ def _load(path: str) -> ctypes.CDLL:
                                   ctypes.c_float], ctypes.c_int),
         "coli_spec_guard_step": ([ctypes.POINTER(SpecGuardC), i32, i32, ctypes.c_double], i32),
     }
+    sig.update({
+        "coli_quant_act_token": ([i32, _P, i64, i32, i32, _P, _P, _P], ctypes.c_int),
+        "coli_swiglu_quant_token": ([i32, _P, i64, _P, i64, i32, i32, _P, _P, _P], ctypes.c_int),
+        "coli_gemm_q8": ([_P, _P, i32, _P, _P, i32, i32, _P, i32, _P, i64, _P], ctypes.c_int),
+        "coli_gemm_q8_grouped": ([_P, _P, i32, _P, _P, i32, i32, i32, _P, _P, i32, i32, i32, _P,
+                                  i64, _P], ctypes.c_int),
+        "coli_moe_combine": ([i32, _P, i64, _P, _P, i32, i32, i32, _P, i64, _P, i64, _P],
+                             ctypes.c_int),
+        "coli_moe_route_scored": ([ctypes.POINTER(ScoreCfg), i32, _P, i64, _P, i32, _P, _P, _P],
+                                  ctypes.c_int),
+    })
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -261,6 +282,172 @@ def coli_moe_dispatch(idx: torch.Tensor, E: int, counts, offs, perm, uniq, n_uni
         _ptr(idx, torch.int32, "idx"), T, k, E, _ptr(counts, torch.int32, "counts"),
         _ptr(offs, torch.int32, "offs"), _ptr(perm, torch.int32, "perm"),
         _ptr(uniq, torch.int32, "uniq"), _ptr(n_uniq, torch.int32, "n_uniq"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit products with one scale per token and one per output channel, and the
+# router over softmax or sigmoid scores.  Activations and results are fp32,
+# bf16 or fp16; their rows may be strided (a slice of a wider buffer).  Every
+# tensor must be on the current device, where the stream is.
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16}
+
+
+def _dense(t, dtype, numel, dev, name):
+    """Address of a contiguous tensor of ``numel`` elements on device ``dev``."""
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, dtype, numel, dev, name)
+    return t.data_ptr()
+
+
+def _refuse(t, dtype, numel, dev, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+
+
+def _rowed(t, rows, cols, dtype, dev, name):
+    """(address, row stride) of a [rows, cols] tensor whose rows are dense."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device")
+    st0, st1 = t.stride()
+    if (st1 != 1 and cols > 1) or (st0 < cols and rows > 1):
+        raise ValueError(f"{name} must have consecutive elements in rows that do not overlap")
+    return t.data_ptr(), max(st0, cols)
+
+
+def _device_of(t, name):
+    """The index of ``t``'s device, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")
+    return dev
+
+
+def _float_type(t, name):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def score_cfg(n_experts, top_k, n_group=1, topk_group=1, score=SCORE_SIGMOID,
+              group_score=GROUP_TOP2, norm_topk_prob=1, routed_scaling_factor=1.0) -> ScoreCfg:
+    return ScoreCfg(n_experts, top_k, n_group, topk_group, score, group_score, norm_topk_prob,
+                    routed_scaling_factor)
+
+
+def coli_moe_route_scored(cfg: ScoreCfg, logits: torch.Tensor, bias: torch.Tensor | None,
+                          idx: torch.Tensor, w: torch.Tensor, stream=None) -> None:
+    """logits [T, E] (any float type, rows may be strided), bias fp32 [E] or None
+    -> idx int32 [T, k] (-1: no expert left), w fp32 [T, k]."""
+    dev = _device_of(logits, "logits")
+    T, E, k = logits.shape[0], cfg.n_experts, cfg.top_k
+    dt = _float_type(logits, "logits")
+    lp, ld = _rowed(logits, T, E, logits.dtype, dev, "logits")
+    _check("coli_moe_route_scored", lib().coli_moe_route_scored(
+        ctypes.byref(cfg), dt, lp, ld,
+        None if bias is None else _dense(bias, torch.float32, E, dev, "bias"), T,
+        _dense(idx, torch.int32, T * k, dev, "idx"), _dense(w, torch.float32, T * k, dev, "w"),
+        _raw_stream(stream)))
+
+
+def coli_quant_act_token(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """x [T, n] (any float type, rows may be strided) -> q int8 [T, n], s fp32 [T]."""
+    dev = _device_of(x, "x")
+    T, n = x.shape
+    dt = _float_type(x, "x")
+    xp, ld = _rowed(x, T, n, x.dtype, dev, "x")
+    _check("coli_quant_act_token", lib().coli_quant_act_token(
+        dt, xp, ld, T, n, _dense(q, torch.int8, T * n, dev, "q"),
+        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream)))
+
+
+def coli_swiglu_quant_token(g: torch.Tensor, u: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
+                            stream=None) -> None:
+    """g, u [T, n] (one float type, rows may be strided) -> q int8 [T, n], s fp32
+    [T] of silu(g) * u."""
+    dev = _device_of(g, "g")
+    T, n = g.shape
+    dt = _float_type(g, "g")
+    gp, ldg = _rowed(g, T, n, g.dtype, dev, "g")
+    up, ldu = _rowed(u, T, n, g.dtype, dev, "u")
+    _check("coli_swiglu_quant_token", lib().coli_swiglu_quant_token(
+        dt, gp, ldg, up, ldu, T, n, _dense(q, torch.int8, T * n, dev, "q"),
+        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream)))
+
+
+def coli_gemm_q8(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+                 y: torch.Tensor, bias: torch.Tensor | None = None, stream=None) -> None:
+    """q int8 [T, K], s fp32 [T], w uint8 [N, K] int8 codes, ws fp32 [N], bias
+    fp32 [N] or None -> y [T, N] (any float type, rows may be strided)."""
+    dev = _device_of(q, "q")
+    T, K = q.shape
+    N = w.shape[0]
+    dt = _float_type(y, "y")
+    yp, ld = _rowed(y, T, N, y.dtype, dev, "y")
+    _check("coli_gemm_q8", lib().coli_gemm_q8(
+        _dense(q, torch.int8, T * K, dev, "q"), _dense(s, torch.float32, T, dev, "s"), T,
+        _dense(w, torch.uint8, N * K, dev, "w"), _dense(ws, torch.float32, N, dev, "ws"), N, K,
+        None if bias is None else _dense(bias, torch.float32, N, dev, "bias"), dt, yp, ld,
+        _raw_stream(stream)))
+
+
+def coli_gemm_q8_grouped(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+                         offs: torch.Tensor, perm: torch.Tensor, y: torch.Tensor, fan: int = 1,
+                         stream=None) -> None:
+    """The experts' products over coli_moe_dispatch's tables: q int8 [R, K], s
+    fp32 [R], w uint8 [E, N, K], ws fp32 [E, N], offs int32 [E + 1], perm int32
+    [P] -> row p of y [P, N] = row p // fan of q times p's expert's weights.
+    Rows of pairs that no expert has are left as they are."""
+    dev = _device_of(q, "q")
+    R, K = q.shape
+    E, N = w.shape[0], w.shape[1]
+    P = perm.numel()
+    dt = _float_type(y, "y")
+    yp, ld = _rowed(y, P, N, y.dtype, dev, "y")
+    _check("coli_gemm_q8_grouped", lib().coli_gemm_q8_grouped(
+        _dense(q, torch.int8, R * K, dev, "q"), _dense(s, torch.float32, R, dev, "s"), R,
+        _dense(w, torch.uint8, E * N * K, dev, "w"),
+        _dense(ws, torch.float32, E * N, dev, "ws"), E, N, K,
+        _dense(offs, torch.int32, E + 1, dev, "offs"), _dense(perm, torch.int32, P, dev, "perm"),
+        P, fan, dt, yp, ld, _raw_stream(stream)))
+
+
+def coli_moe_combine(o: torch.Tensor, idx: torch.Tensor | None, w: torch.Tensor, y: torch.Tensor,
+                     add: torch.Tensor | None = None, stream=None) -> None:
+    """y [T, H] = add + sum_j w[:, j] * o[t * k + j] over the slots whose idx is
+    not negative; o [T * k, H], idx int32 [T, k] or None, w fp32 [T, k], add
+    [T, H] or None (all of one float type; rows may be strided)."""
+    dev = _device_of(o, "o")
+    T, k = w.shape
+    H = y.shape[1]
+    dt = _float_type(y, "y")
+    op, ldo = _rowed(o, T * k, H, y.dtype, dev, "o")
+    yp, ldy = _rowed(y, T, H, y.dtype, dev, "y")
+    ap, lda = (None, 0) if add is None else _rowed(add, T, H, y.dtype, dev, "add")
+    _check("coli_moe_combine", lib().coli_moe_combine(
+        dt, op, ldo, None if idx is None else _dense(idx, torch.int32, T * k, dev, "idx"),
+        _dense(w, torch.float32, T * k, dev, "w"), T, k, H, ap, lda, yp, ldy,
+        _raw_stream(stream)))
 
 
 class MoeLayer:

@@ -11,12 +11,15 @@
 
 #include "coli_moe.h"
 #include "kernels.hpp"
+#include "q8.hpp"
 
 namespace {
 
 
 constexpr int kMaxDim = 8192;
 constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxPairs = 1 << 25;   // kMaxTokens tokens of 32 experts
+constexpr int kMaxQ8Cols = 131040;   // 128 * 128 * K < 2^31: the int32 sums are exact
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -46,6 +49,14 @@ coli_status check_device() {
 }
 
 coli_status from_hip(hipError_t e) { return e == hipSuccess ? COLI_OK : COLI_ERR_DEVICE; }
+
+bool dtype_ok(int d) { return d == COLI_F32 || d == COLI_BF16 || d == COLI_F16; }
+size_t dtype_size(int d) { return d == COLI_F32 ? 4 : 2; }
+
+// rows of `n` elements of type d at p with row stride ld
+bool rows_ok(int d, const void *p, int64_t ld, int64_t n) {
+  return p && aligned(p, dtype_size(d)) && ld >= n && ld <= (int64_t)1 << 40;
+}
 
 bool qtype_ok(int q) { return q == COLI_Q8 || q == COLI_Q4 || q == COLI_Q2; }
 
@@ -392,6 +403,118 @@ coli_status coli_moe_forward_profiled(const coli_moe_layer *L, const float *x, i
                                       void *const *stage_events, int32_t n_stage_events) {
   return forward_impl(L, nullptr, x, T, logits_in, y, idx_out, w_out, logits_out, workspace,
                       workspace_bytes, stream, stage_events, n_stage_events);
+}
+
+coli_status coli_quant_act_token(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t n,
+                                 int8_t *q, float *s, void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || n <= 0 || n % 32 || n > kMaxQ8Cols)
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!rows_ok(dtype, x, ldx, n) || !q || !s || !aligned(q, 16) || !aligned(s, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_quant_token(dtype, x, ldx, nullptr, 0, T, n, q, s,
+                                             static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg, const void *u,
+                                    int64_t ldu, int32_t T, int32_t n, int8_t *q, float *s,
+                                    void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxPairs || n <= 0 || n % 32 || n > kMaxQ8Cols)
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!rows_ok(dtype, g, ldg, n) || !rows_ok(dtype, u, ldu, n) || !q || !s || !aligned(q, 16) ||
+        !aligned(s, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_quant_token(dtype, g, ldg, u, ldu, T, n, q, s,
+                                             static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T, const uint8_t *w, const float *ws,
+                         int32_t N, int32_t K, const float *bias, int32_t dtype, void *y, int64_t ldy,
+                         void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || N < 1 || K <= 0 || K % 32 || K > kMaxQ8Cols)
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!q || !s || !w || !ws || !rows_ok(dtype, y, ldy, N)) return COLI_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(s, 4) || !aligned(ws, 4) || !aligned(bias, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli::Q8Args a{q, s, w, ws, bias, y, ldy, T, N, K, 1, nullptr, nullptr, 0, 1};
+    if (!coli::gemm_q8_fits(a)) return COLI_ERR_UNSUPPORTED;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_gemm_q8(dtype, a, static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_gemm_q8_grouped(const int8_t *q, const float *s, int32_t rows, const uint8_t *w,
+                                 const float *ws, int32_t E, int32_t N, int32_t K,
+                                 const int32_t *offs, const int32_t *perm, int32_t P, int32_t fan,
+                                 int32_t dtype, void *y, int64_t ldy, void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || rows < 0 || P < 0 || P > kMaxPairs || E < 1 || E > 1024 || fan < 1 ||
+        N < 1 || K <= 0 || K % 32 || K > kMaxQ8Cols || (P > 0 && rows < 1))
+      return COLI_ERR_INVALID_ARG;
+    if (P == 0) return COLI_OK;
+    if (!q || !s || !w || !ws || !offs || !perm || !rows_ok(dtype, y, ldy, N))
+      return COLI_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(s, 4) || !aligned(ws, 4) ||
+        !aligned(offs, 4) || !aligned(perm, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli::Q8Args a{q, s, w, ws, nullptr, y, ldy, rows, N, K, E, offs, perm, P, fan};
+    if (!coli::gemm_q8_fits(a)) return COLI_ERR_UNSUPPORTED;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_gemm_q8(dtype, a, static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_moe_combine(int32_t dtype, const void *o, int64_t ldo, const int32_t *idx,
+                             const float *w, int32_t T, int32_t k, int32_t H, const void *add,
+                             int64_t ldadd, void *y, int64_t ldy, void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || k < 1 || k > 32 || H < 1 || H > 131072)
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!rows_ok(dtype, o, ldo, H) || !rows_ok(dtype, y, ldy, H) || !w || !aligned(w, 4) ||
+        !aligned(idx, 4) || (add && !rows_ok(dtype, add, ldadd, H)))
+      return COLI_ERR_INVALID_ARG;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_combine_rows(dtype, o, ldo, idx, w, T, k, H, add, ldadd, y, ldy,
+                                              static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_moe_route_scored(const coli_score_cfg *cfg, int32_t dtype, const void *logits,
+                                  int64_t ld, const float *bias, int32_t T, int32_t *topk_idx,
+                                  float *topk_w, void *stream) {
+  return guarded([&] {
+    if (!cfg || !dtype_ok(dtype) || T < 0 || T > kMaxTokens) return COLI_ERR_INVALID_ARG;
+    const coli_router_cfg shape{cfg->n_experts, cfg->top_k, cfg->n_group, cfg->topk_group,
+                                cfg->norm_topk_prob, cfg->routed_scaling_factor, 0.f, 0};
+    if (!router_ok(&shape) || (cfg->score != COLI_SCORE_SIGMOID && cfg->score != COLI_SCORE_SOFTMAX) ||
+        (cfg->group_score != COLI_GROUP_TOP2 && cfg->group_score != COLI_GROUP_MAX))
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!rows_ok(dtype, logits, ld, cfg->n_experts) || !topk_idx || !topk_w || !aligned(bias, 4) ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    const coli::ScoreCfg c{cfg->n_experts, cfg->top_k, cfg->n_group, cfg->topk_group, cfg->score,
+                           cfg->group_score, cfg->norm_topk_prob, cfg->routed_scaling_factor};
+    return from_hip(coli::launch_route_scored(dtype, c, logits, ld, bias, T, topk_idx, topk_w,
+                                              static_cast<hipStream_t>(stream)));
+  });
 }
 
 }  // extern "C"

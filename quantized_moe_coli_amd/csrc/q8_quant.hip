@@ -1,0 +1,244 @@
+// q8_quant.hip -- int8 codes with one scale per token (row), of a row of
+// activations or of SwiGLU's result, and the weighted sum of a token's
+// expert outputs.
+//
+// A row's codes: a = max|x|, s = fl32(a / 127), q = clamp(round_half_even(
+// fl32(x / s)), -127, 127); s = 0 gives q = 0.  This is the rule of the
+// library's other containers with the row as the block.  A row that holds a
+// NaN or an infinity has no scale: s = NaN and q = 0, so that every product
+// made from it is NaN and the fault stays visible.
+//
+// SwiGLU's h = silu(g) * u is evaluated in binary64 and rounded once to
+// binary32, as the layer's own gate/up kernels do, so that a code next to a
+// rounding border does not depend on how the exponential was approximated.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "q8.hpp"
+
+#pragma clang fp contract(off)
+
+namespace coli {
+namespace {
+
+constexpr int kPiece = 8;    // elements per load
+constexpr int kPieces = 4;   // pieces a thread keeps in registers
+constexpr int kGridX = 1 << 20;  // workgroups along x (a launch's threads along one axis fit 32 bits)
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const double gd = (double)g;
+  return (float)(gd / (1.0 + exp(-gd)) * (double)u);
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_piece(const typename Elem<DT>::type *p, float *v) {
+  typedef typename Elem<DT>::type T;
+  if constexpr (VEC) {
+    constexpr int N = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kPiece / N; ++i) {
+      const Pack<T, N> pk = reinterpret_cast<const Pack<T, N> *>(p)[i];
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i * N + j] = (float)pk.v[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) v[j] = (float)p[j];
+  }
+}
+
+// Codes of one piece, with the row's scale and its reciprocal.  x * inv
+// differs from the correctly rounded x / s by less than 127 * 2^-22, so
+// rounding it to a whole number gives the same code unless it lies within
+// that of a half; there, and for scales too small for a reciprocal (inv =
+// 0), the division is made.
+__device__ __forceinline__ void codes(const float *v, float s, float inv, uint32_t *out) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) {
+    float r = v[j] * inv;
+    float c = rintf(r);
+    if (fabsf(r - c) > 0.4999f || inv == 0.f) c = rintf(v[j] / s);
+    c = fminf(fmaxf(c, -127.f), 127.f);
+    w[j >> 2] |= ((uint32_t)(int32_t)c & 0xFFu) << (8 * (j & 3));
+  }
+  out[0] = w[0];
+  out[1] = w[1];
+}
+
+// A row by TR threads (64, 256 or 1024), in workgroups of at least 256.  Rows of up to kPieces * TR pieces are read once
+// and held in registers between the maximum and the codes; longer ones are
+// read again.
+template <int DT, bool GLU, bool VEC, int TR>
+__global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_quant_token(
+    const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
+    const typename Elem<DT>::type *__restrict__ u, int64_t ldu, int T, int n,
+    int8_t *__restrict__ q, float *__restrict__ s) {
+  constexpr int RPB = TR < 256 ? 256 / TR : 1;
+  __shared__ int part[TR / 64];
+  const int row = (blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TR;
+  if (row >= T) return;  // whole waves (TR >= 64): no barrier is missed, rows of TR > 64 have their own workgroup
+  const int tr = threadIdx.x % TR;
+  const int np = n / kPiece;
+  const auto *xr = x + (int64_t)row * ldx;
+  const auto *ur = GLU ? u + (int64_t)row * ldu : nullptr;
+
+  auto get = [&](int p, float *v) {
+    load_piece<DT, VEC>(xr + (int64_t)p * kPiece, v);
+    if constexpr (GLU) {
+      float w[kPiece];
+      load_piece<DT, VEC>(ur + (int64_t)p * kPiece, w);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) v[j] = silu_mul(v[j], w[j]);
+    }
+  };
+  // |x| as its bits: ordered as the values are, infinities and NaN above
+  // every finite one
+  float v[kPieces][kPiece];
+  int amax = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int p = i * TR + tr;
+    if (p < np) {
+      get(p, v[i]);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) amax = max(amax, __float_as_int(v[i][j]) & 0x7fffffff);
+    }
+  }
+  for (int p = kPieces * TR + tr; p < np; p += TR) {
+    float t[kPiece];
+    get(p, t);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) amax = max(amax, __float_as_int(t[j]) & 0x7fffffff);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) amax = max(amax, __shfl_xor(amax, d, 64));
+  if constexpr (TR > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = amax;
+    __syncthreads();
+    amax = part[0];
+#pragma unroll
+    for (int i = 1; i < TR / 64; ++i) amax = max(amax, part[i]);
+  }
+  const bool bad = amax >= 0x7f800000;
+  const float sc = bad ? __int_as_float(0x7fc00000) : __int_as_float(amax) / 127.f;
+  const float inv = sc > 1e-30f ? 1.f / sc : 0.f;  // 0: divide
+  if (tr == 0) s[row] = sc;
+  const bool zero = bad || sc == 0.f;
+  int8_t *qr = q + (int64_t)row * n;
+  auto put = [&](int p, const float *t) {
+    uint32_t w[2] = {0, 0};
+    if (!zero) codes(t, sc, inv, w);
+    *reinterpret_cast<uint2 *>(qr + (int64_t)p * kPiece) = make_uint2(w[0], w[1]);
+  };
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int p = i * TR + tr;
+    if (p < np) put(p, v[i]);
+  }
+  for (int p = kPieces * TR + tr; p < np; p += TR) {
+    float t[kPiece];
+    get(p, t);
+    put(p, t);
+  }
+}
+
+// y[t][h] = (add[t][h]) + sum_j w[t][j] o[t k + j][h], slots in order, in
+// binary32, rounded once to the type.  A slot whose idx is -1 is not read:
+// its row of o may hold anything.
+template <int DT, int N>
+__global__ __launch_bounds__(256) void k_combine_rows(
+    const typename Elem<DT>::type *__restrict__ o, int64_t ldo, const int32_t *__restrict__ idx,
+    const float *__restrict__ w, int k, int H, const typename Elem<DT>::type *add, int64_t ldadd,
+    typename Elem<DT>::type *y, int64_t ldy) {
+  typedef typename Elem<DT>::type T;
+  const int t = blockIdx.x;
+  const int h = (blockIdx.y * 256 + threadIdx.x) * N;
+  if (h >= H) return;
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  if (add) {
+    const Pack<T, N> a = *reinterpret_cast<const Pack<T, N> *>(add + (int64_t)t * ldadd + h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = (float)a.v[i];
+  }
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = (int64_t)t * k + j;
+    if (idx && idx[p] < 0) continue;
+    const float wj = w[p];
+    const Pack<T, N> a = *reinterpret_cast<const Pack<T, N> *>(o + p * ldo + h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = fmaf(wj, (float)a.v[i], acc[i]);
+  }
+  Pack<T, N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.v[i] = (T)acc[i];
+  *reinterpret_cast<Pack<T, N> *>(y + (int64_t)t * ldy + h) = r;
+}
+
+template <int DT>
+bool rows_aligned(const void *p, int64_t ld, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 &&
+         (uint64_t)ld * sizeof(typename Elem<DT>::type) % bytes == 0;
+}
+
+}  // namespace
+
+hipError_t launch_quant_token(int dt, const void *x, int64_t ldx, const void *u, int64_t ldu, int T,
+                              int n, int8_t *q, float *s, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  return by_dtype(dt, [&](auto dtc) {
+    constexpr int DT = decltype(dtc)::value;
+    typedef typename Elem<DT>::type E;
+    const E *xe = static_cast<const E *>(x), *ue = static_cast<const E *>(u);
+    const bool vec = rows_aligned<DT>(x, ldx, 16) && (!u || rows_aligned<DT>(u, ldu, 16));
+    auto go = [&](auto glu, auto vecc, auto trc) {
+      constexpr int TR = decltype(trc)::value;
+      constexpr int NT = TR < 256 ? 256 : TR, RPB = NT / TR;
+      const int wgs = (T + RPB - 1) / RPB;
+      hipLaunchKernelGGL((k_quant_token<DT, decltype(glu)::value, decltype(vecc)::value, TR>),
+                         dim3(std::min(wgs, kGridX), (wgs + kGridX - 1) / kGridX), dim3(NT), 0, st, xe,
+                         ldx, ue, ldu, T, n, q, s);
+    };
+    auto by_len = [&](auto glu, auto vecc) {
+      if (n <= 64 * kPieces * kPiece) go(glu, vecc, std::integral_constant<int, 64>());
+      else if (n <= 256 * kPieces * kPiece) go(glu, vecc, std::integral_constant<int, 256>());
+      else go(glu, vecc, std::integral_constant<int, 1024>());
+    };
+    auto by_vec = [&](auto glu) {
+      if (vec) by_len(glu, std::true_type());
+      else by_len(glu, std::false_type());
+    };
+    if (u) by_vec(std::true_type());
+    else by_vec(std::false_type());
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_combine_rows(int dt, const void *o, int64_t ldo, const int32_t *idx, const float *w,
+                               int T, int k, int H, const void *add, int64_t ldadd, void *y,
+                               int64_t ldy, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  return by_dtype(dt, [&](auto dtc) {
+    constexpr int DT = decltype(dtc)::value;
+    typedef typename Elem<DT>::type E;
+    constexpr int N = 16 / (int)sizeof(E);
+    auto go = [&](auto nc) {
+      constexpr int NN = decltype(nc)::value;
+      const int per_row = (H + 256 * NN - 1) / (256 * NN);
+      hipLaunchKernelGGL((k_combine_rows<DT, NN>), dim3(T, per_row), dim3(256), 0, st,
+                         static_cast<const E *>(o), ldo, idx, w, k, H, static_cast<const E *>(add),
+                         ldadd, static_cast<E *>(y), ldy);
+    };
+    if (H % N == 0 && rows_aligned<DT>(o, ldo, 16) && rows_aligned<DT>(y, ldy, 16) &&
+        (!add || rows_aligned<DT>(add, ldadd, 16)))
+      go(std::integral_constant<int, N>());
+    else
+      go(std::integral_constant<int, 1>());
+    return hipGetLastError();
+  });
+}
+
+}  // namespace coli
