@@ -268,10 +268,18 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_q8_stream(Q8Args a, int n
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens.  A workgroup of WM x WN waves takes BM tokens and BN
-// channels, each wave BM / WM by BN / WN of them in 32 x 32 products.  k
-// goes by stages of 128 bytes of every row, two stages of LDS: while one is
-// multiplied the next is loaded, and one barrier a stage separates them.
+// Many tokens.  A workgroup of WM x WN waves takes up to BM tokens and BN
+// channels in 32 x 32 products: wave (wm, wn) the token groups of 32 wm, wm +
+// WM, ... and BN / WN consecutive channels.  A tile with fewer tokens (an
+// expert's, or the last) runs the same loop over fewer groups, TMV for each
+// wave, so that its cost follows its tokens and the LDS they leave free holds
+// more stages.
+//
+// k goes by stages of 128 bytes of every row through a ring of STAGES in LDS,
+// filled by direct loads.  The operands of a step (k = 32) are read from LDS
+// while the step before is multiplied, across stages too: before a stage's
+// last step, one barrier both publishes the next stage and frees this one,
+// so there is one barrier a stage and none of its wait is exposed.
 //
 // LDS: a row's stage is 8 pieces of 16 bytes, piece p of row r at place
 // p ^ ((r / 2) % 8), so the 16 rows that 16 lanes read at one k lie in
@@ -282,20 +290,222 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_q8_stream(Q8Args a, int n
 // ---------------------------------------------------------------------------
 constexpr int kStageBytes = 128;
 
-template <int DT, int BM, int BN, int WM, int WN, bool GROUPED>
-__device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn) {
+// s_waitcnt vmcnt(N) lgkmcnt(0) and a barrier.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+struct TileKernel {
   typedef typename Elem<DT>::type T;
-  constexpr int NW = WM * WN;
-  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;  // 32 x 32 products of a wave
-  constexpr int ROWS = BM + BN;
-  constexpr int LD = ROWS / 8 / NW;  // load instructions of a wave in a stage (8 rows each)
-  static_assert(ROWS % (8 * NW) == 0, "whole loads");
-  __shared__ __align__(16) unsigned char ring[2][ROWS * kStageBytes];
+  static constexpr int NW = WM * WN;
+  static constexpr int TN = BN / WN / 32;       // channel groups of a wave
+  static constexpr int TMAX = BM / WM / 32;     // token groups of a wave, at most
+  static constexpr int LW = BN / 8 / NW;        // weight loads of a wave in a stage (8 rows each)
+  static_assert(BN % (8 * NW) == 0 && (32 * WM) % (8 * NW) == 0, "whole loads");
 
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  const Q8Args &a;
+  const Tile &t;
+  unsigned char *ring;   // LDS bytes
+  const int *rows;       // [BM] output rows of the tile's tokens (-1: none)
 
+  template <int TMV>
+  __device__ __forceinline__ void run() {
+    constexpr int XROWS = 32 * WM * TMV;
+    constexpr int LX = XROWS / 8 / NW, NL = LX + LW;
+    constexpr int STAGE = (XROWS + BN) * kStageBytes;
+    constexpr int STAGES = LDS / STAGE < 4 ? LDS / STAGE : 4;
+    static_assert(STAGES >= 2, "ring");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int n0 = t.nb * BN;
+    const int pieces = a.K / 16, full = pieces / 8, stages = (pieces + 7) / 8;
+
+    // this lane's source of each load: row 8 (i NW + wave) + lane / 8 (tokens
+    // first, then weights), piece (lane % 8) ^ key of the row
+    const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.q) + (GROUPED ? 0 : (size_t)t.r0 * a.K);
+    const uint8_t *wb = a.w + ((size_t)t.e * a.N + n0) * a.K;
+    uint32_t off[NL], pl[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int j = i * NW + wave, r = 8 * j + lane / 8;  // XROWS is a multiple of 16: keys go on
+      pl[i] = (lane & 7) ^ (4 * (j & 1) + (lane >> 4));
+      int src;
+      if (i < LX) {
+        const int tt = min(r, t.n - 1);
+        src = GROUPED ? in_row<GROUPED>(a, rows[tt]) : tt;
+      } else {
+        src = min(r - XROWS, a.N - 1 - n0);
+      }
+      off[i] = (uint32_t)src * (uint32_t)a.K;
+    }
+    auto issue = [&](int c) {
+      unsigned char *buf = ring + (c % STAGES) * STAGE;
+      // (opaque: kept as a scalar base and the lane's 32-bit offset)
+      uint64_t xc = reinterpret_cast<uint64_t>(xb) + (uint64_t)c * kStageBytes;
+      uint64_t wc = reinterpret_cast<uint64_t>(wb) + (uint64_t)c * kStageBytes;
+      asm("" : "+s"(xc), "+s"(wc));
+      const uint32_t last = c < full ? 7 : (uint32_t)(pieces - 8 * c - 1);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t o = off[i] + 16 * min(pl[i], last);
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t *>(i < LX ? xc : wc) + o,
+                                         (lds_void *)(buf + (i * NW + wave) * 1024), 16, 0, 0);
+      }
+    };
+
+    v16i acc[TN][TMV];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TMV; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+    const int lr = lane & 31, lh = lane >> 5, key = (lr >> 1) & 7;
+    struct Ops {
+      v4i x[TMV], w[TN];
+    };
+    auto read = [&](int c, int ks, Ops &o) {
+      const unsigned char *buf = ring + (c % STAGES) * STAGE + lr * kStageBytes + 16 * ((2 * ks + lh) ^ key);
+#pragma unroll
+      for (int j = 0; j < TMV; ++j)
+        o.x[j] = *reinterpret_cast<const v4i *>(buf + (j * WM + wm) * 32 * kStageBytes);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        o.w[i] = *reinterpret_cast<const v4i *>(buf + (XROWS + (wn * TN + i) * 32) * kStageBytes);
+    };
+    auto mul = [&](const Ops &o) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TMV; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[i], o.x[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+
+    Ops A, B;
+#pragma unroll
+    for (int c = 0; c < STAGES; ++c)
+      if (c < stages) issue(c);
+    if (stages >= STAGES) stage_barrier<NL *(STAGES - 1)>();
+    else stage_barrier<0>();
+    read(0, 0, A);
+    for (int c = 0; c < full; ++c) {
+      read(c, 1, B);
+      mul(A);
+      read(c, 2, A);
+      mul(B);
+      read(c, 3, B);
+      mul(A);
+      // stage c + 1 has landed for every wave, and no wave reads stage c any more
+      if (c + STAGES <= stages) stage_barrier<NL *(STAGES - 2)>();
+      else stage_barrier<0>();
+      if (c + 1 < stages) read(c + 1, 0, A);
+      if (c + STAGES < stages) issue(c + STAGES);
+      mul(B);
+    }
+    // the part of a stage that is left (K is a multiple of 32)
+    if (full < stages) {
+      const int steps = (pieces - 8 * full) / 2;
+      mul(A);
+      for (int ks = 1; ks < steps; ++ks) {
+        read(full, ks, A);
+        mul(A);
+      }
+    }
+    finish_tile<TMV>(acc, wave, wm, wn, n0);
+  }
+
+  // y from the accumulators: lane (lr, lh) holds token lr of each group and
+  // channels 8 g + 4 lh + 0..3 (g < 4) of each 32.  Each wave turns its 32
+  // tokens x 32 TN channels at a time in an LDS area of its own, so that a
+  // store writes whole runs of a row.
+  template <int TMV>
+  __device__ __forceinline__ void finish_tile(const v16i (*acc)[TMV], int wave, int wm, int wn, int n0) {
+    constexpr int ROWB = 32 * TN * (int)sizeof(T);  // bytes of a row in the area
+    constexpr int CH = ROWB / 16;                   // 16-byte chunks in it
+    constexpr int EPC = 16 / (int)sizeof(T);        // elements of a chunk
+    static_assert(NW * 32 * ROWB <= LDS, "area");
+    const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+    const int nw = n0 + wn * TN * 32;
+    const float *ws = a.ws + (size_t)t.e * a.N;
+    float sn[TN][16], bn[TN][16];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int n = min(nw + 32 * i + 8 * (r / 4) + 4 * lh + r % 4, a.N - 1);
+        sn[i][r] = ws[n];
+        bn[i][r] = a.bias ? a.bias[n] : 0.f;
+      }
+    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (uint64_t)a.ldy * sizeof(T) % 16 == 0;
+    stage_barrier<0>();  // every wave has read its last operands
+    unsigned char *area = ring + wave * 32 * ROWB;
+    T *y = static_cast<T *>(a.y);
+#pragma unroll
+    for (int j = 0; j < TMV; ++j) {
+      const int t0 = (j * WM + wm) * 32;
+      if (t0 >= t.n) break;
+      const int mine = rows[min(t0 + lr, t.n - 1)];
+      const float st = a.s[in_row<GROUPED>(a, mine)];
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          Pack<T, 4> v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v.v[r] = (T)finish(acc[i][j][4 * g + r], st, sn[i][4 * g + r], bn[i][4 * g + r]);
+          const int e = 32 * i + 8 * g + 4 * lh;  // first element: chunk e / EPC, the key swaps chunks
+          *reinterpret_cast<Pack<T, 4> *>(area + lr * ROWB + (((e / EPC) ^ (lr & 7)) * 16) +
+                                          (e % EPC) * (int)sizeof(T)) = v;
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (vec) {
+#pragma unroll
+        for (int p = 0; p < 32 * CH / 64; ++p) {
+          const int rr = p * (64 / CH) + lane / CH, ch = lane % CH;
+          const Pack<T, EPC> v = *reinterpret_cast<const Pack<T, EPC> *>(area + rr * ROWB + ((ch ^ (rr & 7)) * 16));
+          const int n = nw + ch * EPC;
+          if (t0 + rr >= t.n || n >= a.N) continue;
+          const int row = rows[t0 + rr];
+          if (row < 0) continue;
+          T *d = y + (int64_t)row * a.ldy + n;
+          if (n + EPC <= a.N) {
+            *reinterpret_cast<Pack<T, EPC> *>(d) = v;
+          } else {
+#pragma unroll
+            for (int k = 0; k < EPC - 1; ++k)
+              if (n + k < a.N) d[k] = v.v[k];
+          }
+        }
+      } else {
+        for (int rr = 0; rr < 32 && t0 + rr < t.n; ++rr) {
+          const int row = rows[t0 + rr];
+          if (row < 0) continue;
+#pragma unroll
+          for (int e = 0; e < 32 * TN; e += 64) {
+            const int k = e + lane;
+            if (k < 32 * TN && nw + k < a.N)
+              y[(int64_t)row * a.ldy + nw + k] = *reinterpret_cast<const T *>(
+                  area + rr * ROWB + (((k / EPC) ^ (rr & 7)) * 16) + (k % EPC) * (int)sizeof(T));
+          }
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+};
+
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+__device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows) {
   Tile t;
   if constexpr (GROUPED) {
     const Experts x = scan_experts<BM>(a);
@@ -306,111 +516,28 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn) {
   } else {
     const int id = xcd_item(blockIdx.x, nbm * nbn);
     if (id < 0) return;
-    // runs of 8 token tiles: the workgroups of an XCD at one time share
+    // runs of 4 token tiles: the workgroups of an XCD at one time share
     // about as many token rows as weight rows
-    const int run = 8 * nbn, g = id / run, h = min(8, nbm - g * 8);
-    const int m = g * 8 + (id % run) % h;
+    const int run = 4 * nbn, g = id / run, h = min(4, nbm - g * 4);
+    const int m = g * 4 + (id % run) % h;
     t = Tile{0, m * BM, min(BM, a.rows - m * BM), (id % run) / h};
   }
-  const int n0 = t.nb * BN;
-  const int pieces = a.K / 16;
-  const uint8_t *wb = a.w + (size_t)t.e * a.N * a.K;
-
-  // this lane's source of each load: row 8 (i NW + wave) + lane / 8 of the
-  // tile (tokens first), piece (lane % 8) ^ key
-  const uint8_t *src[LD];
-#pragma unroll
-  for (int i = 0; i < LD; ++i) {
-    const int r = 8 * (i * NW + wave) + lane / 8;
-    if (r < BM) {
-      const int pos = t.r0 + min(r, t.n - 1);
-      src[i] = reinterpret_cast<const uint8_t *>(a.q) +
-               (size_t)in_row<GROUPED>(a, out_row<GROUPED>(a, pos)) * a.K;
-    } else {
-      src[i] = wb + (size_t)min(n0 + r - BM, a.N - 1) * a.K;
-    }
-  }
-  // (BM is a multiple of 16, so the key of a row is the same counted from BM)
-  const int pl = (lane & 7) ^ ((lane >> 4) & 3);  // key = (r / 2) % 8; r = 8 j + lane / 8
-  auto issue = [&](int c) {
-    unsigned char *buf = ring[c & 1];
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int j = i * NW + wave;                 // group of 8 rows
-      const int p = c * 8 + (pl ^ (4 * (j & 1)));  // rows 8 j ..: key = 4 (j % 2) + (lane / 16)
-      __builtin_amdgcn_global_load_lds(src[i] + 16 * (size_t)min(p, pieces - 1),
-                                       (lds_void *)(buf + (size_t)j * 1024), 16, 0, 0);
-    }
-  };
-
-  v16i acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-
-  const int lr = lane & 31, lh = lane >> 5;
-  const int key = (lr >> 1) & 7;
-  auto step = [&](const unsigned char *buf, int ks) {
-    v4i x[TM], w[TN];
-    const int p = 16 * ((2 * ks + lh) ^ key);
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-      x[j] = *reinterpret_cast<const v4i *>(buf + (wm * TM * 32 + 32 * j + lr) * kStageBytes + p);
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-      w[i] = *reinterpret_cast<const v4i *>(buf + (BM + wn * TN * 32 + 32 * i + lr) * kStageBytes + p);
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], x[j], acc[i][j], 0, 0, 0);
-  };
-
-  const int stages = (pieces + 7) / 8;
-  issue(0);
-  for (int c = 0; c < stages; ++c) {
-    // this wave's loads of stage c have landed; past the barrier every
-    // wave's have, and every wave is done with the other buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (c + 1 < stages) issue(c + 1);
-    const unsigned char *buf = ring[c & 1];
-    const int left = pieces - c * 8;
-    if (left >= 8) {
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) step(buf, ks);
-    } else {
-      for (int ks = 0; ks < left / 2; ++ks) step(buf, ks);  // K is a multiple of 32
-    }
-  }
-
-  // lane: token lr of each 32, channels 8 g + 4 lh + 0..3 (g < 4) of each 32
-  T *y = static_cast<T *>(a.y);
-  const float *ws = a.ws + (size_t)t.e * a.N;
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int tt = wm * TM * 32 + 32 * j + lr;
-    if (tt >= t.n) continue;
-    const int row = out_row<GROUPED>(a, t.r0 + tt);
-    if (row < 0) continue;
-    const float st = a.s[in_row<GROUPED>(a, row)];
-    T *yr = y + (int64_t)row * a.ldy;
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int n = n0 + wn * TN * 32 + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
-        if (n < a.N) yr[n] = (T)finish(acc[i][j][r], st, ws[n], a.bias ? a.bias[n] : 0.f);
-      }
-  }
+  for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
+  __syncthreads();
+  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED> k{a, t, ring, rows};
+  constexpr int TMAX = BM / WM / 32;
+  const int tm = (t.n + 32 * WM - 1) / (32 * WM);
+  if (TMAX >= 4 && tm >= 4) k.template run<TMAX < 4 ? TMAX : 4>();
+  else if (TMAX >= 3 && tm == 3) k.template run<TMAX < 3 ? TMAX : 3>();
+  else if (tm == 2) k.template run<2>();
+  else k.template run<1>();
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int OCC, bool GROUPED>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void k_q8_tile(Q8Args a, int nbm, int nbn) {
-  tile_body<DT, BM, BN, WM, WN, GROUPED>(a, nbm, nbn);
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_q8_tile(Q8Args a, int nbm, int nbn) {
+  __shared__ __align__(16) unsigned char ring[LDS];
+  __shared__ int rows[BM];
+  tile_body<DT, BM, BN, WM, WN, LDS, GROUPED>(a, nbm, nbn, ring, rows);
 }
 
 // Upper bound of the token tiles of BM over E experts with P pairs.
@@ -430,6 +557,7 @@ Variant variant_of(const Q8Args &a) {
   if (avg <= 12) return kStream1;
   if (avg <= 28) return kStream2;
   if (avg <= 64) return kStream4;
+  if (a.offs) return kTile256;
   if (avg < 1024) return kTile128;
   return kTile256;
 }
@@ -451,20 +579,22 @@ void run_stream(const Q8Args &a, int64_t wgs, hipStream_t st) {
                        dim3(64 * kStreamWaves), 0, st, a, nbn);
 }
 
-template <int DT, int BM, int BN, int WM, int WN>
+template <int DT, int BM, int BN, int WM, int WN, int LDS>
 void run_tile(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
   if (a.offs)
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, 2, true>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
+    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, LDS, true>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
                        nbm, nbn);
   else
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, 2, false>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
+    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, LDS, false>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
                        nbm, nbn);
 }
 
 }  // namespace
 
 bool gemm_q8_fits(const Q8Args &a) {
+  // (the grouped tiles name rows of q by 32-bit byte offsets)
+  if (a.offs && (int64_t)a.rows * a.K >= (int64_t)1 << 32) return false;
   const Variant v = variant_of(a);
   return workgroups(a, v) * kShapes[v].threads < ((int64_t)1 << 31);
 }
@@ -479,8 +609,8 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
       case kStream1: run_stream<DT, 1, 1>(a, wgs, st); break;
       case kStream2: run_stream<DT, 2, 1>(a, wgs, st); break;
       case kStream4: run_stream<DT, 4, 2>(a, wgs, st); break;
-      case kTile128: run_tile<DT, 128, 128, 2, 2>(a, wgs, st); break;
-      case kTile256: run_tile<DT, 256, 256, 2, 4>(a, wgs, st); break;
+      case kTile128: run_tile<DT, 128, 128, 2, 2, 64 << 10>(a, wgs, st); break;
+      case kTile256: run_tile<DT, 256, 256, 2, 4, 144 << 10>(a, wgs, st); break;
     }
     return hipGetLastError();
   });
