@@ -15,10 +15,10 @@
 // operand, so a lane's results are one token's consecutive channels.
 //
 // Two kernels:
-//   k_q8_stream  few tokens (per expert): bound by reading the weights.  They
-//                go from memory to registers in operand order, with no LDS.
-//   k_q8_tile    many tokens: bound by the matrix cores.  Tiles of both
-//                operands go to LDS by direct loads, double-buffered.
+//   k_q8_ring   few tokens (per expert): bound by reading the weights.  Many
+//               small stages of both operands are in flight.
+//   k_q8_tile   many tokens: bound by the matrix cores.  Large tiles, each
+//               operand read from LDS once for several products.
 #include <type_traits>
 
 #include "q8.hpp"
@@ -93,14 +93,16 @@ __device__ __forceinline__ Experts scan_experts(const Q8Args &a) {
   // (offs that are no running sum could count more tiles than there are)
   const int bound = a.P / BM + min(a.P, a.E);
   mine = min(mine, bound);
+  // inclusive sum over the lanes: row shifts by 1, 2, 4, 8, then rows' totals
   int sum = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(sum, d, 64);
-    if (lane >= d) sum += o;
-  }
+  sum += dpp_i32<0x111>(sum);
+  sum += dpp_i32<0x112>(sum);
+  sum += dpp_i32<0x114>(sum);
+  sum += dpp_i32<0x118>(sum);
+  sum += dpp_i32<0x142, 0xA>(sum);
+  sum += dpp_i32<0x143, 0xC>(sum);
   x.before = sum - mine;
-  x.total = min(__shfl(sum, 63, 64), bound);
+  x.total = min(__builtin_amdgcn_readlane(sum, 63), bound);
   return x;
 }
 
@@ -128,14 +130,10 @@ __device__ __forceinline__ Tile find_tile(const Q8Args &a, const Experts &x, int
       b = nx;
     }
   }
-  t.e = __shfl(r.x, owner, 64);
-  t.r0 = __shfl(r.y, owner, 64);
-  t.n = __shfl(r.z, owner, 64);
-  t.nb = __shfl(r.w, owner, 64);
-  t.e = __builtin_amdgcn_readfirstlane(t.e);
-  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
-  t.n = __builtin_amdgcn_readfirstlane(t.n);
-  t.nb = __builtin_amdgcn_readfirstlane(t.nb);
+  t.e = __builtin_amdgcn_readlane(r.x, owner);
+  t.r0 = __builtin_amdgcn_readlane(r.y, owner);
+  t.n = __builtin_amdgcn_readlane(r.z, owner);
+  t.nb = __builtin_amdgcn_readlane(r.w, owner);
   return t;
 }
 
@@ -152,119 +150,196 @@ __device__ __forceinline__ float finish(int acc, float st, float sn, float b) {
   return (float)acc * (st * sn) + b;
 }
 
-// ---------------------------------------------------------------------------
-// Few tokens.  A workgroup of 8 waves takes 16 NT channels and up to 16 MT
-// tokens; the waves take the 128-byte chunks of k in turn and their exact
-// partial sums are added through LDS.
-// ---------------------------------------------------------------------------
-constexpr int kStreamWaves = 8;
+// s_waitcnt vmcnt(N) lgkmcnt(0) and a barrier.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
-template <int DT, int MT, int NT, bool GROUPED>
-__global__ __launch_bounds__(64 * kStreamWaves) void k_q8_stream(Q8Args a, int nbn) {
+// ---------------------------------------------------------------------------
+// Few tokens.  A workgroup takes up to BM tokens and BN channels: WM x WN
+// waves share them out, and KS such sets share out k, whose exact partial
+// sums are added through LDS at the end.  k goes by stages of 256 bytes of
+// every row through a ring of STAGES in LDS, filled by direct loads, of which
+// all but the one being multiplied are in flight; one barrier a stage both
+// publishes the oldest and frees the one before it.
+//
+// Loads of whole 256-byte runs of rows are what this kernel is about: read
+// straight into operand registers (64 bytes of 16 rows an instruction) the
+// tokens' codes cost more than the weights from 16 tokens on (6144 x 6144,
+// one launch after another: 1 token 9.1 us against 7.3 here, 16 tokens 10.4
+// against 7.6, 61 tokens 18.8 against 10.1).
+//
+// LDS: a row's stage is 16 pieces of 16 bytes, piece p of row r at place p ^
+// (r % 16): 16 lanes that read 16 rows at one k meet all 64 banks.
+// ---------------------------------------------------------------------------
+constexpr int kRingBytes = 256;
+constexpr int kRingPieces = kRingBytes / 16;
+
+template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, bool GROUPED>
+struct RingKernel {
   typedef typename Elem<DT>::type T;
-  __shared__ int part[kStreamWaves][MT * NT][4][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int li = lane & 15, lg = lane >> 4;
+  static constexpr int NW = WM * WN * KS;
+  static constexpr int ROWS = BM + BN;
+  static constexpr int NL = ROWS / 4 / NW;  // loads of a wave in a stage (4 rows each)
+  static constexpr int STAGE = ROWS * kRingBytes;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+  static constexpr int STEPS = 4 / KS;      // steps of k = 64 of a wave in a stage
+  static constexpr int PART = KS * BM * BN * 4;
+  static constexpr int LDS = STAGES * STAGE > PART ? STAGES * STAGE : PART;
+  static_assert(ROWS % (4 * NW) == 0 && BM % 4 == 0 && 4 % KS == 0, "whole loads and steps");
 
+  __device__ __forceinline__ static void run(const Q8Args &a, const Tile &t, unsigned char *ring,
+                                             const int *rows) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int wm = wave % WM, wn = (wave / WM) % WN, kq = wave / (WM * WN);
+    const int n0 = t.nb * BN;
+    const int pieces = a.K / 16, full = pieces / kRingPieces;
+    const int stages = (pieces + kRingPieces - 1) / kRingPieces;
+
+    // this lane's source of each load: row 4 (i NW + wave) + lane / 16
+    // (tokens first), piece (lane % 16) ^ (row % 16)
+    const uint8_t *src[NL];
+    uint32_t pl[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = (i * NW + wave) * 4 + lane / 16;
+      pl[i] = (lane & 15) ^ (r & 15);
+      if ((i * NW + wave) * 4 < BM) {
+        const int tt = min(r, t.n - 1);
+        const int row = GROUPED ? in_row<GROUPED>(a, rows[tt]) : t.r0 + tt;
+        src[i] = reinterpret_cast<const uint8_t *>(a.q) + (size_t)row * a.K;
+      } else {
+        src[i] = a.w + ((size_t)t.e * a.N + min(n0 + r - BM, a.N - 1)) * a.K;
+      }
+    }
+    auto issue = [&](int c) {
+      unsigned char *buf = ring + (c % STAGES) * STAGE;
+      const uint32_t last = c < full ? kRingPieces - 1 : (uint32_t)(pieces - kRingPieces * c - 1);
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        __builtin_amdgcn_global_load_lds(src[i] + (size_t)c * kRingBytes + 16 * min(pl[i], last),
+                                         (lds_void *)(buf + (i * NW + wave) * 1024), 16, 0, 0);
+    };
+
+    v4i acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+    // step s (k = 64 s ..) of a stage; a part stage's pieces past the row's
+    // end count as zero weights
+    auto step = [&](const unsigned char *buf, int s, int left) {
+      const int p = 4 * s + lg;
+      v4i x[TM], w[TN];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int r = (wm * TM + j) * 16 + li;
+        x[j] = *reinterpret_cast<const v4i *>(buf + r * kRingBytes + 16 * (p ^ li));
+      }
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const int r = BM + (wn * TN + i) * 16 + li;
+        w[i] = *reinterpret_cast<const v4i *>(buf + r * kRingBytes + 16 * (p ^ li));
+        if (left < kRingPieces) w[i] = p < left ? w[i] : v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], x[j], acc[i][j], 0, 0, 0);
+    };
+
+#pragma unroll
+    for (int c = 0; c < STAGES - 1; ++c)
+      if (c < stages) issue(c);
+    for (int c = 0; c < stages; ++c) {
+      // stage c has landed for every wave, and no wave reads stage c - 1 any more
+      if (c + STAGES - 1 <= stages) stage_barrier<NL *(STAGES - 2)>();
+      else stage_barrier<0>();
+      if (c + STAGES - 1 < stages) issue(c + STAGES - 1);
+      const unsigned char *buf = ring + (c % STAGES) * STAGE;
+      if (c < full) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) step(buf, kq * STEPS + s, kRingPieces);
+      } else {
+        const int left = pieces - kRingPieces * c;
+        for (int s = 0; s < STEPS; ++s)
+          if (4 * (kq * STEPS + s) < left) step(buf, kq * STEPS + s, left);
+      }
+    }
+
+    stage_barrier<0>();
+    int *part = reinterpret_cast<int *>(ring);
+    constexpr int TILES = (BM / 16) * (BN / 16);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int tl = (wm * TM + j) * (BN / 16) + wn * TN + i;
+        *reinterpret_cast<v4i *>(part + (kq * TILES + tl) * 256 + 4 * lane) = acc[i][j];
+      }
+    __syncthreads();
+    // lane: token li, channels 4 lg .. of a 16 x 16 product
+    T *y = static_cast<T *>(a.y);
+    const bool vec = reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(T)) == 0 && a.ldy % 4 == 0;
+    for (int tl = wave; tl < TILES; tl += NW) {
+      const int tt = (tl / (BN / 16)) * 16 + li, n = n0 + (tl % (BN / 16)) * 16 + 4 * lg;
+      if (tt >= t.n || n >= a.N) continue;
+      const int row = GROUPED ? rows[tt] : t.r0 + tt;
+      if (row < 0) continue;
+      v4i sum = *reinterpret_cast<const v4i *>(part + tl * 256 + 4 * lane);
+#pragma unroll
+      for (int k = 1; k < KS; ++k)
+        sum += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
+      const float st = a.s[in_row<GROUPED>(a, row)];
+      const float *ws = a.ws + (size_t)t.e * a.N;
+      Pack<T, 4> v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int nr = min(n + r, a.N - 1);
+        v.v[r] = (T)finish(sum[r], st, ws[nr], a.bias ? a.bias[nr] : 0.f);
+      }
+      T *d = y + (int64_t)row * a.ldy + n;
+      if (vec && n + 4 <= a.N) {
+        *reinterpret_cast<Pack<T, 4> *>(d) = v;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.N) d[r] = v.v[r];
+      }
+    }
+  }
+};
+
+template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(Q8Args a, int nbm, int nbn) {
+  typedef RingKernel<DT, BM, BN, WM, WN, KS, STAGES, GROUPED> K;
+  __shared__ __align__(16) unsigned char ring[K::LDS];
+  __shared__ int rows[GROUPED ? BM : 1];
   Tile t;
   if constexpr (GROUPED) {
-    const Experts x = scan_experts<16 * MT>(a);
+    const Experts x = scan_experts<BM>(a);
     const int id = xcd_item(blockIdx.x, x.total * nbn);
     if (id < 0) return;
-    t = find_tile<16 * MT>(a, x, id, nbn);
+    t = find_tile<BM>(a, x, id, nbn);
     if (t.n <= 0) return;
+    if (threadIdx.x < t.n) rows[threadIdx.x] = out_row<GROUPED>(a, t.r0 + threadIdx.x);
+    __syncthreads();
   } else {
-    t = Tile{0, (int)blockIdx.y * 16 * MT, min(16 * MT, a.rows - (int)blockIdx.y * 16 * MT),
-             (int)blockIdx.x};
+    const int id = xcd_item(blockIdx.x, nbm * nbn);
+    if (id < 0) return;
+    const int m = id % nbm;  // the token tiles of a channel block are neighbours
+    t = Tile{0, m * BM, min(BM, a.rows - m * BM), id / nbm};
   }
-  const int n0 = t.nb * 16 * NT;
-  const uint8_t *wb = a.w + (size_t)t.e * a.N * a.K;
-  const uint8_t *wp[NT];
-  const int8_t *xp[MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) wp[i] = wb + (size_t)min(n0 + 16 * i + li, a.N - 1) * a.K;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int pos = t.r0 + min(16 * i + li, t.n - 1);
-    xp[i] = a.q + (size_t)in_row<GROUPED>(a, out_row<GROUPED>(a, pos)) * a.K;
-  }
-  v4i acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-
-  const int pieces = a.K / 16, full = pieces / 8;
-  auto mul = [&](const v4i (&wv)[2][NT], const v4i (&xv)[2][MT]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[h][i], xv[h][j], acc[i][j], 0, 0, 0);
-  };
-  // U chunks' loads are in flight together
-  constexpr int U = MT * NT == 1 ? 6 : MT + NT <= 4 ? 3 : 2;
-  int c = wave;
-  for (; c + (U - 1) * kStreamWaves < full; c += U * kStreamWaves) {
-    v4i wv[U][2][NT], xv[U][2][MT];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const size_t o = (size_t)(c + u * kStreamWaves) * 128 + 64 * h + 16 * lg;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          wv[u][h][i] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[i] + o));
-#pragma unroll
-        for (int i = 0; i < MT; ++i) xv[u][h][i] = *reinterpret_cast<const v4i *>(xp[i] + o);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u) mul(wv[u], xv[u]);
-  }
-  // what is left, and the part chunk at the row's end: pieces past it count
-  // as zero weights
-  for (; c * 8 < pieces; c += kStreamWaves) {
-    v4i wv[2][NT], xv[2][MT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int pc = c * 8 + 4 * h + lg;
-      const size_t o = (size_t)min(pc, pieces - 1) * 16;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const v4i v = *reinterpret_cast<const v4i *>(wp[i] + o);
-        wv[h][i] = pc < pieces ? v : v4i{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xv[h][i] = *reinterpret_cast<const v4i *>(xp[i] + o);
-    }
-    mul(wv, xv);
-  }
-
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][j * NT + i][r][lane] = acc[i][j][r];
-  __syncthreads();
-  T *y = static_cast<T *>(a.y);
-  for (int o = threadIdx.x; o < 256 * MT * NT; o += 64 * kStreamWaves) {
-    const int nn = o % (16 * NT), tt = o / (16 * NT);
-    const int n = n0 + nn;
-    if (tt >= t.n || n >= a.N) continue;
-    const int row = out_row<GROUPED>(a, t.r0 + tt);
-    if (row < 0) continue;
-    const int tile = (tt / 16) * NT + nn / 16, l = tt % 16 + 16 * ((nn % 16) / 4);
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kStreamWaves; ++w) sum += part[w][tile][nn % 4][l];
-    const float b = a.bias ? a.bias[n] : 0.f;
-    y[(int64_t)row * a.ldy + n] =
-        (T)finish(sum, a.s[in_row<GROUPED>(a, row)], a.ws[(size_t)t.e * a.N + n], b);
-  }
+  K::run(a, t, ring, rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -289,16 +364,6 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_q8_stream(Q8Args a, int n
 // bring in is never used.
 // ---------------------------------------------------------------------------
 constexpr int kStageBytes = 128;
-
-// s_waitcnt vmcnt(N) lgkmcnt(0) and a barrier.
-template <int N>
-__device__ __forceinline__ void stage_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
 struct TileKernel {
@@ -546,17 +611,18 @@ int64_t max_tiles(const Q8Args &a, int bm) { return a.P / bm + (a.P < a.E ? a.P 
 // The variants, by the tokens (for each expert, on average) that share a
 // weight row: few tokens stream the weights, more take tiles that are as
 // large as still leave enough of them.
-enum Variant { kStream1, kStream2, kStream4, kTile128, kTile256 };
+enum Variant { kRing16, kRing32, kRing64, kRing64Wide, kTile128, kTile256 };
 struct Shape {
   int bm, bn, threads;
 };
-constexpr Shape kShapes[] = {{16, 16, 512}, {32, 16, 512}, {64, 32, 512}, {128, 128, 256}, {256, 256, 512}};
+constexpr Shape kShapes[] = {{16, 32, 256},  {32, 64, 256},   {64, 32, 512},
+                             {64, 128, 512}, {128, 128, 256}, {256, 256, 512}};
 
 Variant variant_of(const Q8Args &a) {
   const int64_t avg = a.offs ? ((int64_t)a.P + a.E - 1) / a.E : a.rows;
-  if (avg <= 12) return kStream1;
-  if (avg <= 28) return kStream2;
-  if (avg <= 64) return kStream4;
+  if (avg <= (a.offs ? 12 : 16)) return kRing16;
+  if (avg <= (a.offs ? 24 : 32)) return kRing32;
+  if (avg <= (a.offs ? 56 : 64)) return a.offs ? kRing64Wide : kRing64;
   if (a.offs) return kTile256;
   if (avg < 1024) return kTile128;
   return kTile256;
@@ -569,14 +635,14 @@ int64_t workgroups(const Q8Args &a, Variant v) {
   return (nbm * nbn + 7) / 8 * 8;
 }
 
-template <int DT, int MT, int NT>
-void run_stream(const Q8Args &a, int64_t wgs, hipStream_t st) {
-  const int nbn = (a.N + 16 * NT - 1) / (16 * NT);
+template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES>
+void run_ring(const Q8Args &a, int64_t wgs, hipStream_t st) {
+  const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
+  constexpr int NT = 64 * WM * WN * KS;
   if (a.offs)
-    hipLaunchKernelGGL((k_q8_stream<DT, MT, NT, true>), dim3(wgs), dim3(64 * kStreamWaves), 0, st, a, nbn);
+    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, true>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
   else
-    hipLaunchKernelGGL((k_q8_stream<DT, MT, NT, false>), dim3(nbn, (a.rows + 16 * MT - 1) / (16 * MT)),
-                       dim3(64 * kStreamWaves), 0, st, a, nbn);
+    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, false>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
 }
 
 template <int DT, int BM, int BN, int WM, int WN, int LDS>
@@ -606,9 +672,10 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     switch (v) {
-      case kStream1: run_stream<DT, 1, 1>(a, wgs, st); break;
-      case kStream2: run_stream<DT, 2, 1>(a, wgs, st); break;
-      case kStream4: run_stream<DT, 4, 2>(a, wgs, st); break;
+      case kRing16: run_ring<DT, 16, 32, 1, 1, 4, 6>(a, wgs, st); break;
+      case kRing32: run_ring<DT, 32, 64, 1, 1, 4, 3>(a, wgs, st); break;
+      case kRing64: run_ring<DT, 64, 32, 2, 1, 4, 6>(a, wgs, st); break;
+      case kRing64Wide: run_ring<DT, 64, 128, 2, 2, 2, 3>(a, wgs, st); break;
       case kTile128: run_tile<DT, 128, 128, 2, 2, 64 << 10>(a, wgs, st); break;
       case kTile256: run_tile<DT, 256, 256, 2, 4, 144 << 10>(a, wgs, st); break;
     }
