@@ -17,4 +17,7 @@ def __getattr__(name):
         return importlib.import_module("." + name, __name__)
     if name.startswith("__"):
         raise AttributeError(name)
-    return getattr(importlib.import_module(".binding", __name__), name)
+    value = getattr(importlib.import_module(".binding", __name__), name)
+    if callable(value):  # functions and classes: later accesses are plain lookups
+        globals()[name] = value
+    return value

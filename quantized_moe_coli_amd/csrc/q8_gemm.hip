@@ -58,40 +58,38 @@ __device__ __forceinline__ int in_row(const Q8Args &a, int out) {
   else return out;
 }
 
-// The grouped product's tile number `id` among (expert, channel block, token
-// tile): each wave sums the experts' tile counts itself (E <= 1024, at most
-// 16 a lane), so no table and no extra launch is needed.  The grid is the
-// host's bound; `total` is what there is to do.  Token tiles of one expert
-// and channel block are neighbours, so that their weights are read from
-// memory once.
-struct Experts {
-  int lo, hi;    // this lane's experts
-  int before;    // token tiles of the experts before them
-  int total;     // token tiles of all experts
-};
-
-__device__ __forceinline__ int expert_begin(const Q8Args &a, int e) {
-  return min(max(a.offs[e], 0), a.P);
+// Workgroup b runs on XCD b % 8, each with its own L2: an XCD takes a
+// contiguous run of the `total` items, so that neighbours share it.
+__device__ __forceinline__ int xcd_item(int b, int total) {
+  const int per = (total + 7) / 8;
+  const int i = (b % 8) * per + b / 8;
+  return b / 8 < per && i < total ? i : -1;
 }
 
-template <int BM>
-__device__ __forceinline__ Experts scan_experts(const Q8Args &a) {
+// The grouped product's tile of this workgroup among (expert, channel block,
+// token tile).  Each wave sums the experts' tile counts itself (E <= 1024, at
+// most 16 a lane, all loaded at once), so no table and no extra launch is
+// needed.  The grid is the host's bound; workgroups past the experts' tiles
+// get t.n = 0.  Token tiles of one expert and channel block are neighbours, so
+// that their weights are read from memory once.
+template <int BM, int EPL>
+__device__ __forceinline__ Tile expert_tile_n(const Q8Args &a, int nbn) {
   const int lane = threadIdx.x & 63;
   const int per = (a.E + 63) / 64;
-  Experts x;
-  x.lo = min(lane * per, a.E);
-  x.hi = min(x.lo + per, a.E);
-  int mine = 0;
-  if (x.lo < x.hi) {
-    int b = expert_begin(a, x.lo);
-    for (int e = x.lo; e < x.hi; ++e) {
-      const int nx = expert_begin(a, e + 1);
-      if (nx > b) mine += (nx - b + BM - 1) / BM;
-      b = nx;
-    }
-  }
+  const int lo = lane * per;
+  int o[EPL + 1];
+#pragma unroll
+  for (int i = 0; i <= EPL; ++i)
+    if (i <= per) o[i] = a.offs[min(lo + i, a.E)];
   // (offs that are no running sum could count more tiles than there are)
   const int bound = a.P / BM + min(a.P, a.E);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i <= EPL; ++i)
+    if (i <= per) {
+      o[i] = min(max(o[i], 0), a.P);
+      if (i > 0 && o[i] > o[i - 1]) mine += (o[i] - o[i - 1] + BM - 1) / BM;
+    }
   mine = min(mine, bound);
   // inclusive sum over the lanes: row shifts by 1, 2, 4, 8, then rows' totals
   int sum = mine;
@@ -101,48 +99,37 @@ __device__ __forceinline__ Experts scan_experts(const Q8Args &a) {
   sum += dpp_i32<0x118>(sum);
   sum += dpp_i32<0x142, 0xA>(sum);
   sum += dpp_i32<0x143, 0xC>(sum);
-  x.before = sum - mine;
-  x.total = min(__builtin_amdgcn_readlane(sum, 63), bound);
-  return x;
-}
-
-// The tile `id` of `x.total * nbn`; id is uniform.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const Q8Args &a, const Experts &x, int id, int nbn) {
-  const int lane = threadIdx.x & 63;
-  // the last lane whose first tile is not past id holds it, if it has any
-  const uint64_t le = __ballot((int64_t)x.before * nbn <= id && x.lo < x.hi);
-  const int owner = 63 - __clzll(le);
+  const int total = min(__builtin_amdgcn_readlane(sum, 63), bound);
+  const int id = xcd_item(blockIdx.x, total * nbn);
   Tile t{0, 0, 0, 0};
-  int4 r = make_int4(0, 0, 0, 0);
-  if (lane == owner) {
-    int before = x.before, b = expert_begin(a, x.lo);
-    for (int e = x.lo; e < x.hi; ++e) {
-      const int nx = expert_begin(a, e + 1);
-      const int mt = nx > b ? (nx - b + BM - 1) / BM : 0;
-      if ((int64_t)(before + mt) * nbn > id) {
-        const int local = (int)(id - (int64_t)before * nbn);
-        const int m = local % mt;
-        r = make_int4(e, b + m * BM, min(BM, nx - b - m * BM), local / mt);
-        break;
+  if (id < 0) return t;
+  int before = sum - mine;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (i < per) {
+      const int n = o[i + 1] - o[i], mt = n > 0 ? (n + BM - 1) / BM : 0;
+      const int64_t local = id - (int64_t)before * nbn;
+      if (!found && local >= 0 && local < (int64_t)mt * nbn) {
+        found = true;
+        const int l = (int)local, nb = mt == 1 ? l : l / mt, m = l - nb * mt;
+        t = Tile{lo + i, o[i] + m * BM, min(BM, n - m * BM), nb};
       }
       before += mt;
-      b = nx;
     }
-  }
-  t.e = __builtin_amdgcn_readlane(r.x, owner);
-  t.r0 = __builtin_amdgcn_readlane(r.y, owner);
-  t.n = __builtin_amdgcn_readlane(r.z, owner);
-  t.nb = __builtin_amdgcn_readlane(r.w, owner);
+  const uint64_t who = __ballot(found);
+  if (!who) return Tile{0, 0, 0, 0};
+  const int owner = __builtin_ctzll(who);
+  t.e = __builtin_amdgcn_readlane(t.e, owner);
+  t.r0 = __builtin_amdgcn_readlane(t.r0, owner);
+  t.n = __builtin_amdgcn_readlane(t.n, owner);
+  t.nb = __builtin_amdgcn_readlane(t.nb, owner);
   return t;
 }
 
-// Workgroup b runs on XCD b % 8, each with its own L2: an XCD takes a
-// contiguous run of the `total` items, so that neighbours share it.
-__device__ __forceinline__ int xcd_item(int b, int total) {
-  const int per = (total + 7) / 8;
-  const int i = (b % 8) * per + b / 8;
-  return b / 8 < per && i < total ? i : -1;
+template <int BM>
+__device__ __forceinline__ Tile expert_tile(const Q8Args &a, int nbn) {
+  return a.E <= 256 ? expert_tile_n<BM, 4>(a, nbn) : expert_tile_n<BM, 16>(a, nbn);
 }
 
 // y's element from the exact sum.
@@ -326,10 +313,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(Q8Args a, int nbm
   __shared__ int rows[GROUPED ? BM : 1];
   Tile t;
   if constexpr (GROUPED) {
-    const Experts x = scan_experts<BM>(a);
-    const int id = xcd_item(blockIdx.x, x.total * nbn);
-    if (id < 0) return;
-    t = find_tile<BM>(a, x, id, nbn);
+    t = expert_tile<BM>(a, nbn);
     if (t.n <= 0) return;
     if (threadIdx.x < t.n) rows[threadIdx.x] = out_row<GROUPED>(a, t.r0 + threadIdx.x);
     __syncthreads();
@@ -350,29 +334,32 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(Q8Args a, int nbm
 // wave, so that its cost follows its tokens and the LDS they leave free holds
 // more stages.
 //
-// k goes by stages of 128 bytes of every row through a ring of STAGES in LDS,
+// k goes by stages of SB bytes of every row through a ring of STAGES in LDS,
 // filled by direct loads.  The operands of a step (k = 32) are read from LDS
 // while the step before is multiplied, across stages too: before a stage's
 // last step, one barrier both publishes the next stage and frees this one,
 // so there is one barrier a stage and none of its wait is exposed.
 //
-// LDS: a row's stage is 8 pieces of 16 bytes, piece p of row r at place
-// p ^ ((r / 2) % 8), so the 16 rows that 16 lanes read at one k lie in
-// different banks (two rows span the 64 banks).  The loads write LDS in lane
-// order, so the swizzle is in the addresses they read.  Rows past the tile
+// LDS: piece p (16 bytes) of row r's stage lies at place p ^ key(r), so that
+// the 16 rows which 16 lanes read at one k lie in different banks.  The
+// loads write LDS in lane order, so the swizzle is in the addresses they
+// read.  Rows past the tile
 // and pieces past the row's end read valid addresses near them; what they
 // bring in is never used.
 // ---------------------------------------------------------------------------
-constexpr int kStageBytes = 128;
-
-template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
 struct TileKernel {
   typedef typename Elem<DT>::type T;
   static constexpr int NW = WM * WN;
   static constexpr int TN = BN / WN / 32;       // channel groups of a wave
   static constexpr int TMAX = BM / WM / 32;     // token groups of a wave, at most
-  static constexpr int LW = BN / 8 / NW;        // weight loads of a wave in a stage (8 rows each)
-  static_assert(BN % (8 * NW) == 0 && (32 * WM) % (8 * NW) == 0, "whole loads");
+  static constexpr int PPR = SB / 16;           // pieces of a row in a stage
+  static constexpr int RPL = 64 / PPR;          // rows of a load
+  static constexpr int KSN = SB / 32;           // steps of a stage
+  static constexpr int LW = BN / RPL / NW;      // weight loads of a wave in a stage
+  static_assert((SB == 64 || SB == 128 || SB == 256) && BN % (RPL * NW) == 0, "whole loads");
+  // place of piece p of row r: p ^ key(r); 256 / SB rows span the banks
+  __device__ __forceinline__ static int key(int r) { return (r / (256 / SB)) & (PPR - 1); }
 
   const Q8Args &a;
   const Tile &t;
@@ -382,25 +369,35 @@ struct TileKernel {
   template <int TMV>
   __device__ __forceinline__ void run() {
     constexpr int XROWS = 32 * WM * TMV;
-    constexpr int LX = XROWS / 8 / NW, NL = LX + LW;
-    constexpr int STAGE = (XROWS + BN) * kStageBytes;
-    constexpr int STAGES = LDS / STAGE < 4 ? LDS / STAGE : 4;
-    static_assert(STAGES >= 2, "ring");
+    // token loads of a wave: whole ones, and one by half the lanes where the
+    // rows are an odd multiple of what half the loads bring
+    constexpr int LXF = XROWS / (RPL * NW), HALF = XROWS % (RPL * NW) ? 1 : 0;
+    constexpr int LX = LXF + HALF, NL = LX + LW;
+    static_assert(HALF == 0 || XROWS % (RPL * NW) == RPL * NW / 2, "whole or half loads");
+    constexpr int STAGE = (XROWS + BN) * SB;
+    constexpr int STAGES = LDS / STAGE < 6 ? LDS / STAGE : 6;
+    static_assert(STAGES >= 2 && NL * (STAGES - 1) < 64, "ring");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int n0 = t.nb * BN;
-    const int pieces = a.K / 16, full = pieces / 8, stages = (pieces + 7) / 8;
+    const int pieces = a.K / 16, full = pieces / PPR, stages = (pieces + PPR - 1) / PPR;
 
-    // this lane's source of each load: row 8 (i NW + wave) + lane / 8 (tokens
-    // first, then weights), piece (lane % 8) ^ key of the row
+    // this lane's source of each load: its row (tokens first, then weights)
+    // and the piece of it that belongs at its place
     const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.q) + (GROUPED ? 0 : (size_t)t.r0 * a.K);
     const uint8_t *wb = a.w + ((size_t)t.e * a.N + n0) * a.K;
     uint32_t off[NL], pl[NL];
+    // first row of load i in the stage
+    auto row_of = [&](int i) {
+      if (i < LXF) return (i * NW + wave) * RPL;
+      if (i < LX) return LXF * NW * RPL + wave * (RPL / 2);
+      return XROWS + ((i - LX) * NW + wave) * RPL;
+    };
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int j = i * NW + wave, r = 8 * j + lane / 8;  // XROWS is a multiple of 16: keys go on
-      pl[i] = (lane & 7) ^ (4 * (j & 1) + (lane >> 4));
+      const int r = row_of(i) + lane / PPR;
+      pl[i] = (lane % PPR) ^ key(r);
       int src;
       if (i < LX) {
         const int tt = min(r, t.n - 1);
@@ -413,15 +410,16 @@ struct TileKernel {
     auto issue = [&](int c) {
       unsigned char *buf = ring + (c % STAGES) * STAGE;
       // (opaque: kept as a scalar base and the lane's 32-bit offset)
-      uint64_t xc = reinterpret_cast<uint64_t>(xb) + (uint64_t)c * kStageBytes;
-      uint64_t wc = reinterpret_cast<uint64_t>(wb) + (uint64_t)c * kStageBytes;
+      uint64_t xc = reinterpret_cast<uint64_t>(xb) + (uint64_t)c * SB;
+      uint64_t wc = reinterpret_cast<uint64_t>(wb) + (uint64_t)c * SB;
       asm("" : "+s"(xc), "+s"(wc));
-      const uint32_t last = c < full ? 7 : (uint32_t)(pieces - 8 * c - 1);
+      const uint32_t last = c < full ? PPR - 1 : (uint32_t)(pieces - PPR * c - 1);
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const uint32_t o = off[i] + 16 * min(pl[i], last);
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t *>(i < LX ? xc : wc) + o,
-                                         (lds_void *)(buf + (i * NW + wave) * 1024), 16, 0, 0);
+        if (i < LXF || i >= LX || lane < 32)
+          __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t *>(i < LX ? xc : wc) + o,
+                                           (lds_void *)(buf + row_of(i) * SB), 16, 0, 0);
       }
     };
 
@@ -433,18 +431,18 @@ struct TileKernel {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-    const int lr = lane & 31, lh = lane >> 5, key = (lr >> 1) & 7;
+    const int lr = lane & 31, lh = lane >> 5, rkey = key(lr);
     struct Ops {
       v4i x[TMV], w[TN];
     };
     auto read = [&](int c, int ks, Ops &o) {
-      const unsigned char *buf = ring + (c % STAGES) * STAGE + lr * kStageBytes + 16 * ((2 * ks + lh) ^ key);
+      const unsigned char *buf = ring + (c % STAGES) * STAGE + lr * SB + 16 * ((2 * ks + lh) ^ rkey);
 #pragma unroll
       for (int j = 0; j < TMV; ++j)
-        o.x[j] = *reinterpret_cast<const v4i *>(buf + (j * WM + wm) * 32 * kStageBytes);
+        o.x[j] = *reinterpret_cast<const v4i *>(buf + (j * WM + wm) * 32 * SB);
 #pragma unroll
       for (int i = 0; i < TN; ++i)
-        o.w[i] = *reinterpret_cast<const v4i *>(buf + (XROWS + (wn * TN + i) * 32) * kStageBytes);
+        o.w[i] = *reinterpret_cast<const v4i *>(buf + (XROWS + (wn * TN + i) * 32) * SB);
     };
     auto mul = [&](const Ops &o) {
 #pragma unroll
@@ -465,10 +463,13 @@ struct TileKernel {
     for (int c = 0; c < full; ++c) {
       read(c, 1, B);
       mul(A);
-      read(c, 2, A);
-      mul(B);
-      read(c, 3, B);
-      mul(A);
+#pragma unroll
+      for (int ks = 2; ks < KSN; ks += 2) {
+        read(c, ks, A);
+        mul(B);
+        read(c, ks + 1, B);
+        mul(A);
+      }
       // stage c + 1 has landed for every wave, and no wave reads stage c any more
       if (c + STAGES <= stages) stage_barrier<NL *(STAGES - 2)>();
       else stage_barrier<0>();
@@ -478,7 +479,7 @@ struct TileKernel {
     }
     // the part of a stage that is left (K is a multiple of 32)
     if (full < stages) {
-      const int steps = (pieces - 8 * full) / 2;
+      const int steps = (pieces - PPR * full) / 2;
       mul(A);
       for (int ks = 1; ks < steps; ++ks) {
         read(full, ks, A);
@@ -569,14 +570,11 @@ struct TileKernel {
   }
 };
 
-template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
 __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows) {
   Tile t;
   if constexpr (GROUPED) {
-    const Experts x = scan_experts<BM>(a);
-    const int id = xcd_item(blockIdx.x, x.total * nbn);
-    if (id < 0) return;
-    t = find_tile<BM>(a, x, id, nbn);
+    t = expert_tile<BM>(a, nbn);
     if (t.n <= 0) return;
   } else {
     const int id = xcd_item(blockIdx.x, nbm * nbn);
@@ -589,20 +587,20 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, uns
   }
   for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
   __syncthreads();
-  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED> k{a, t, ring, rows};
+  TileKernel<DT, BM, BN, WM, WN, SB, LDS, GROUPED> k{a, t, ring, rows};
   constexpr int TMAX = BM / WM / 32;
   const int tm = (t.n + 32 * WM - 1) / (32 * WM);
   if (TMAX >= 4 && tm >= 4) k.template run<TMAX < 4 ? TMAX : 4>();
   else if (TMAX >= 3 && tm == 3) k.template run<TMAX < 3 ? TMAX : 3>();
-  else if (tm == 2) k.template run<2>();
+  else if (TMAX >= 2 && tm == 2) k.template run<TMAX < 2 ? TMAX : 2>();
   else k.template run<1>();
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_q8_tile(Q8Args a, int nbm, int nbn) {
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
-  tile_body<DT, BM, BN, WM, WN, LDS, GROUPED>(a, nbm, nbn, ring, rows);
+  tile_body<DT, BM, BN, WM, WN, SB, LDS, GROUPED>(a, nbm, nbn, ring, rows);
 }
 
 // Upper bound of the token tiles of BM over E experts with P pairs.
@@ -635,24 +633,24 @@ int64_t workgroups(const Q8Args &a, Variant v) {
   return (nbm * nbn + 7) / 8 * 8;
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES>
+template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, int GSTAGES>
 void run_ring(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
   constexpr int NT = 64 * WM * WN * KS;
   if (a.offs)
-    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, true>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
+    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, GSTAGES, true>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
   else
     hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, false>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int LDS>
+template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS>
 void run_tile(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
   if (a.offs)
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, LDS, true>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
+    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, true>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
                        nbm, nbn);
   else
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, LDS, false>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
+    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, false>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
                        nbm, nbn);
 }
 
@@ -672,12 +670,12 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     switch (v) {
-      case kRing16: run_ring<DT, 16, 32, 1, 1, 4, 6>(a, wgs, st); break;
-      case kRing32: run_ring<DT, 32, 64, 1, 1, 4, 3>(a, wgs, st); break;
-      case kRing64: run_ring<DT, 64, 32, 2, 1, 4, 6>(a, wgs, st); break;
-      case kRing64Wide: run_ring<DT, 64, 128, 2, 2, 2, 3>(a, wgs, st); break;
-      case kTile128: run_tile<DT, 128, 128, 2, 2, 64 << 10>(a, wgs, st); break;
-      case kTile256: run_tile<DT, 256, 256, 2, 4, 144 << 10>(a, wgs, st); break;
+      case kRing16: run_ring<DT, 16, 32, 1, 1, 4, 6, 3>(a, wgs, st); break;
+      case kRing32: run_ring<DT, 32, 64, 1, 1, 4, 3, 3>(a, wgs, st); break;
+      case kRing64: run_ring<DT, 64, 32, 2, 1, 4, 6, 3>(a, wgs, st); break;
+      case kRing64Wide: run_ring<DT, 64, 128, 2, 2, 2, 3, 3>(a, wgs, st); break;
+      case kTile128: run_tile<DT, 128, 128, 2, 2, 128, 64 << 10>(a, wgs, st); break;
+      case kTile256: run_tile<DT, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
     }
     return hipGetLastError();
   });

@@ -8,6 +8,12 @@
 // a group holds its experts l, l + L, ...  The scores are evaluated in
 // binary64 and rounded once to binary32, so neither the order of a sum nor
 // the approximation of an exponential moves an expert past another.
+//
+// Bound by instructions, not by memory: a token's exponentials and the k
+// rounds of its selection.  Reductions go by DPP moves instead of the LDS
+// permutes of __shfl, a round whose best score is unique (a ballot tells)
+// needs no reduction of indices, and the exponential is as exact as the
+// rounding to binary32 needs.
 #include <cmath>
 
 #include "q8.hpp"
@@ -19,53 +25,107 @@ namespace {
 
 constexpr float kOff = -INFINITY;  // score of an expert that cannot be chosen
 
+// exp(x) in binary64: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor
+// series of e^r up to r^11 (the rest is below 2^-47 of the result).  Past
+// +-1100 it is 0 or infinity, whatever x.
+__device__ __forceinline__ double exp_64(double x) {
+  x = __builtin_fmin(__builtin_fmax(x, -1100.0), 1100.0);
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
+  r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);
+  double p = 1.0 / 39916800;
+  p = __builtin_fma(p, r, 1.0 / 3628800);
+  p = __builtin_fma(p, r, 1.0 / 362880);
+  p = __builtin_fma(p, r, 1.0 / 40320);
+  p = __builtin_fma(p, r, 1.0 / 5040);
+  p = __builtin_fma(p, r, 1.0 / 720);
+  p = __builtin_fma(p, r, 1.0 / 120);
+  p = __builtin_fma(p, r, 1.0 / 24);
+  p = __builtin_fma(p, r, 1.0 / 6);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / x for x >= 1, to about 2^-50; 0 for an infinity.
+__device__ __forceinline__ double inverse_64(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  if (x > 1e300) return y;
+  y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+
+// The two largest of (b1 >= b2) and the partner's, by one move of the lanes.
+template <int CTRL>
+__device__ __forceinline__ void top2_step(float &b1, float &b2) {
+  const float o1 = dpp_f32<CTRL>(b1), o2 = dpp_f32<CTRL>(b2);
+  b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+  b1 = fmaxf(b1, o1);
+}
+
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// (dpp moves into lanes outside a row mask bring 0: the smallest of
+// non-negative indices is right in lane 63, which is the one that is read)
+__device__ __forceinline__ int wave_min_index(int v) {
+  v = min(v, dpp_i32<0xB1>(v));
+  v = min(v, dpp_i32<0x4E>(v));
+  v = min(v, dpp_i32<0x141>(v));
+  v = min(v, dpp_i32<0x140>(v));
+  v = min(v, dpp_i32<0x142, 0xA>(v));
+  v = min(v, dpp_i32<0x143, 0xC>(v));
+  return lane_value(v, 63);
+}
+
 template <int DT, int EPL>
-__global__ __launch_bounds__(256) void k_route_scored(
-    ScoreCfg c, const typename Elem<DT>::type *__restrict__ logits, int64_t ld,
-    const float *__restrict__ bias, int T, int L, int32_t *__restrict__ idx_out,
-    float *__restrict__ w_out) {
-  const int t = blockIdx.x * 4 + threadIdx.x / 64;
-  if (t >= T) return;
+__device__ __forceinline__ void route_token(const ScoreCfg &c, const typename Elem<DT>::type *row,
+                                            const float *bias, int L, int32_t *idx_out, float *w_out) {
   const int lane = threadIdx.x & 63;
   const int per = c.E / c.n_group;
   const int g = lane / L, l = lane % L;
-  const auto *row = logits + (int64_t)t * ld;
 
-  float lg[EPL], p[EPL], s[EPL];
-  float top = kOff;
-#pragma unroll
-  for (int m = 0; m < EPL; ++m) {
-    const int i = l + m * L;
-    const bool in = g < c.n_group && i < per;
-    const float v = in ? (float)row[g * per + i] : kOff;
-    lg[m] = v > kOff ? v : kOff;  // NaN: off
-    top = fmaxf(top, lg[m]);
-  }
-  if (c.score == COLI_SCORE_SOFTMAX) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    double e[EPL], sum = 0.0;
+  float p[EPL], s[EPL];
+  {
+    float lg[EPL], b[EPL];
 #pragma unroll
     for (int m = 0; m < EPL; ++m) {
-      // equal infinities share the probability
-      e[m] = lg[m] == kOff ? 0.0 : lg[m] == top ? 1.0 : exp((double)lg[m] - (double)top);
-      sum += e[m];
+      const int i = l + m * L;
+      const bool in = g < c.n_group && i < per;
+      const int e = in ? g * per + i : 0;
+      const float v = (float)row[e];
+      b[m] = bias ? bias[e] : 0.f;
+      lg[m] = in && v > kOff ? v : kOff;  // NaN: off
+    }
+    if (c.score == COLI_SCORE_SOFTMAX) {
+      float top = lg[0];
+#pragma unroll
+      for (int m = 1; m < EPL; ++m) top = fmaxf(top, lg[m]);
+      top = wave_max(top);
+      double e[EPL], sum = 0.0;
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) {
+        // (equal infinities share the probability; -inf - top is no number, and off)
+        e[m] = lg[m] == top ? 1.0 : exp_64((double)lg[m] - (double)top);
+        if (lg[m] == kOff) e[m] = 0.0;
+        sum += e[m];
+      }
+      sum = wave_sum_f64(sum);
+      const double inv = sum >= 1.0 ? inverse_64(sum) : 0.0;
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) p[m] = (float)(e[m] * inv);
+    } else {
+#pragma unroll
+      for (int m = 0; m < EPL; ++m)
+        p[m] = lg[m] == kOff ? 0.f : (float)inverse_64(1.0 + exp_64(-(double)lg[m]));
     }
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-#pragma unroll
-    for (int m = 0; m < EPL; ++m) p[m] = sum > 0.0 ? (float)(e[m] / sum) : 0.f;
-  } else {
-#pragma unroll
-    for (int m = 0; m < EPL; ++m)
-      p[m] = lg[m] == kOff ? 0.f : (float)(1.0 / (1.0 + exp(-(double)lg[m])));
-  }
-#pragma unroll
-  for (int m = 0; m < EPL; ++m) {
-    s[m] = kOff;
-    if (lg[m] > kOff) {
-      const float v = bias ? p[m] + bias[g * per + l + m * L] : p[m];
-      s[m] = v > kOff ? v : kOff;
+    for (int m = 0; m < EPL; ++m) {
+      const float v = bias ? p[m] + b[m] : p[m];
+      s[m] = lg[m] > kOff && v > kOff ? v : kOff;
     }
   }
 
@@ -76,8 +136,12 @@ __global__ __launch_bounds__(256) void k_route_scored(
       b2 = fmaxf(b2, fminf(b1, s[m]));
       b1 = fmaxf(b1, s[m]);
     }
-    for (int d = L >> 1; d >= 1; d >>= 1) {
-      const float o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+    if (L >= 2) top2_step<0xB1>(b1, b2);
+    if (L >= 4) top2_step<0x4E>(b1, b2);
+    if (L >= 8) top2_step<0x141>(b1, b2);
+    if (L >= 16) top2_step<0x140>(b1, b2);
+    if (L >= 32) {
+      const float o1 = __shfl_xor(b1, 16, 64), o2 = __shfl_xor(b2, 16, 64);
       b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
       b1 = fmaxf(b1, o1);
     }
@@ -85,7 +149,7 @@ __global__ __launch_bounds__(256) void k_route_scored(
     // kept if fewer than topk_group groups come before it
     int ahead = 0;
     for (int o = 0; o < c.n_group; ++o) {
-      const float v = __shfl(gs, o * L, 64);
+      const float v = lane_value(gs, o * L);
       ahead += v > gs || (v == gs && o < g);
     }
     if (ahead >= c.topk_group) {
@@ -97,35 +161,33 @@ __global__ __launch_bounds__(256) void k_route_scored(
   int my_idx = -1;
   float my_p = 0.f, total = 0.f;
   for (int j = 0; j < c.k; ++j) {
-    float best = kOff;
-    int at = 0x7fffffff, bm = 0;
+    // this lane's best: its experts are in rising order, the first of equals stays
+    float best = s[0], bp = p[0];
+    int bm = 0;
 #pragma unroll
-    for (int m = 0; m < EPL; ++m) {
-      // a lane's experts are in rising order: the first of equals stays
-      if (s[m] > best) {
-        best = s[m];
-        bm = m;
-        at = g * per + l + m * L;
-      }
+    for (int m = 1; m < EPL; ++m) {
+      const bool more = s[m] > best;
+      best = more ? s[m] : best;
+      bp = more ? p[m] : bp;
+      bm = more ? m : bm;
     }
-    float wb = best;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) wb = fmaxf(wb, __shfl_xor(wb, d, 64));
+    const float wb = wave_max(best);
     if (wb == kOff) break;  // no expert is left
-    int wi = best == wb ? at : 0x7fffffff;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) wi = min(wi, __shfl_xor(wi, d, 64));
-    float pv = 0.f;
-    if (at == wi) {
-#pragma unroll
-      for (int m = 0; m < EPL; ++m)
-        if (m == bm) {
-          pv = p[m];
-          s[m] = kOff;
-        }
+    const int at = g * per + l + bm * L;
+    const uint64_t who = __ballot(best == wb);
+    int owner = __builtin_ctzll(who);
+    int wi;
+    if ((who & (who - 1)) == 0) {
+      wi = lane_value(at, owner);
+    } else {
+      wi = wave_min_index(best == wb ? at : 0x7fffffff);
+      owner = __builtin_ctzll(__ballot(best == wb && at == wi));
     }
-    const int owner = __ffsll(__ballot(at == wi)) - 1;
-    pv = __shfl(pv, owner, 64);
+    const float pv = lane_value(bp, owner);
+    if (lane == owner) {
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) s[m] = m == bm ? kOff : s[m];
+    }
     total += pv;
     if (lane == j) {
       my_idx = wi;
@@ -135,9 +197,22 @@ __global__ __launch_bounds__(256) void k_route_scored(
   if (lane < c.k) {
     float w = my_p;
     if (c.norm) w = total > 0.f ? w / total : 0.f;
-    idx_out[(int64_t)t * c.k + lane] = my_idx;
-    w_out[(int64_t)t * c.k + lane] = my_idx < 0 ? 0.f : w * c.rsf;
+    idx_out[lane] = my_idx;
+    w_out[lane] = my_idx < 0 ? 0.f : w * c.rsf;
   }
+}
+
+constexpr int kRouteWaves = 4;  // tokens of a workgroup
+
+template <int DT, int EPL>
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route_scored(
+    ScoreCfg c, const typename Elem<DT>::type *__restrict__ logits, int64_t ld,
+    const float *__restrict__ bias, int T, int L, int32_t *__restrict__ idx_out,
+    float *__restrict__ w_out) {
+  const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (t >= T) return;
+  route_token<DT, EPL>(c, logits + (int64_t)t * ld, bias, L, idx_out + (int64_t)t * c.k,
+                       w_out + (int64_t)t * c.k);
 }
 
 }  // namespace
@@ -153,8 +228,8 @@ hipError_t launch_route_scored(int dt, const ScoreCfg &c, const void *logits, in
     constexpr int DT = decltype(dtc)::value;
     const auto *lg = static_cast<const typename Elem<DT>::type *>(logits);
     auto go = [&](auto epl) {
-      hipLaunchKernelGGL((k_route_scored<DT, decltype(epl)::value>), dim3((T + 3) / 4), dim3(256), 0, st,
-                         c, lg, ld, bias, T, L, idx, w);
+      hipLaunchKernelGGL((k_route_scored<DT, decltype(epl)::value>), dim3((T + kRouteWaves - 1) / kRouteWaves),
+                         dim3(64 * kRouteWaves), 0, st, c, lg, ld, bias, T, L, idx, w);
     };
     if (need <= 1) go(std::integral_constant<int, 1>());
     else if (need <= 2) go(std::integral_constant<int, 2>());
