@@ -14,9 +14,11 @@
 // k = 16 (lane / 16).  Weight rows are the A operand and tokens the B
 // operand, so a lane's results are one token's consecutive channels.
 //
-// Two kernels:
-//   k_q8_ring   few tokens (per expert): bound by reading the weights.  Many
-//               small stages of both operands are in flight.
+// Three kernels:
+//   k_q8_ring   few tokens: bound by reading the weights, with k split over
+//               the waves so that few channels still fill the chip.
+//   k_q8_sweep  few tokens per expert, many weights: bound by reading them
+//               from memory, straight into operand registers.
 //   k_q8_tile   many tokens: bound by the matrix cores.  Large tiles, each
 //               operand read from LDS once for several products.
 #include <type_traits>
@@ -327,6 +329,286 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(Q8Args a, int nbm
 }
 
 // ---------------------------------------------------------------------------
+// Weights once through, for as many tokens as they are read for (up to BM).
+// A workgroup of NW waves takes 32 NW channels; each wave has 32 of them for
+// itself, so their weights need no LDS: they go from memory to operand
+// registers, D chunks of 128 bytes of k ahead.  The registers of a CU hold
+// several times what its LDS does, and that many bytes have to be in flight
+// for the full rate of the memory.  The tokens' codes, which all waves use,
+// go through a ring of D + 1 chunks in LDS as in the other kernels, with one
+// barrier a chunk.
+//
+// The products are 16 x 16 x 64, MT groups of 16 tokens (as many as the tile
+// has tokens for) by two of 16 channels for each wave.
+// ---------------------------------------------------------------------------
+template <int DT, int BM, int NW, int D, bool GROUPED>
+struct SweepKernel {
+  typedef typename Elem<DT>::type T;
+  static constexpr int BN = 32 * NW;
+  static constexpr int SB = 128, PPR = 8;
+  static constexpr int RINGB = (D + 1) * BM * SB;
+  static constexpr int ROWB = BN * (int)sizeof(T);       // a row of the result area
+  static constexpr int AREAB = 16 * ROWB;
+  static constexpr int LDS = RINGB > AREAB ? RINGB : AREAB;
+  __device__ __forceinline__ static int key(int r) { return (r >> 1) & 7; }
+
+  const Q8Args &a;
+  const Tile &t;
+  unsigned char *ring;
+  const int *rows;
+
+  template <int MT>
+  __device__ __forceinline__ void run() {
+    constexpr int LW = 4;                              // weight loads of a wave in a chunk
+    constexpr int LX = (2 * MT + NW - 1) / NW;         // token loads of a wave (8 rows each)
+    constexpr int XB = 16 * MT * SB;
+    static_assert(D * (LX + LW) < 64, "vmcnt range");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int n0 = t.nb * BN;
+    const int pieces = a.K / 16, full = pieces / PPR, chunks = (pieces + PPR - 1) / PPR;
+
+    const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.q) + (GROUPED ? 0 : (size_t)t.r0 * a.K);
+    const uint8_t *wb = a.w + ((size_t)t.e * a.N + n0) * a.K;
+    uint32_t xoff[LX], xpl[LX], woff[2];
+    // (waves past the last group of 8 rows load that group again)
+    auto xgroup = [&](int i) { return min(i * NW + wave, 2 * MT - 1); };
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+      const int r = 8 * xgroup(i) + lane / 8, tt = min(r, t.n - 1);
+      xpl[i] = (lane & 7) ^ key(r);
+      xoff[i] = (uint32_t)(GROUPED ? in_row<GROUPED>(a, rows[tt]) : tt) * (uint32_t)a.K;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      woff[i] = (uint32_t)min(32 * wave + 16 * i + li, a.N - 1 - n0) * (uint32_t)a.K + 16 * lg;
+
+    auto issue = [&](int c) {
+      unsigned char *buf = ring + (c % (D + 1)) * XB;
+      uint64_t xc = reinterpret_cast<uint64_t>(xb) + (uint64_t)c * SB;
+      asm("" : "+s"(xc));
+      const uint32_t last = c < full ? PPR - 1 : (uint32_t)(pieces - PPR * c - 1);
+#pragma unroll
+      for (int i = 0; i < LX; ++i)
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t *>(xc) + (xoff[i] + 16 * min(xpl[i], last)),
+                                         (lds_void *)(buf + xgroup(i) * 1024), 16, 0, 0);
+    };
+    v4i w[D][2][2];  // [chunk][k half][channel group]
+    auto load = [&](v4i (*v)[2], int c) {
+      uint64_t wc = reinterpret_cast<uint64_t>(wb) + (uint64_t)c * SB;
+      asm("" : "+s"(wc));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[h][i] = *reinterpret_cast<const v4i *>(reinterpret_cast<const uint8_t *>(wc) + woff[i] + 64 * h);
+    };
+    // the part chunk: pieces past the row's end count as zero weights
+    auto load_part = [&](v4i (*v)[2], int c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int p = PPR * c + 4 * h + lg;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const v4i x = *reinterpret_cast<const v4i *>(wb + woff[i] - 16 * lg + 16 * (size_t)min(p, pieces - 1));
+          v[h][i] = p < pieces ? x : v4i{0, 0, 0, 0};
+        }
+      }
+    };
+    v4i acc[2][MT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    // a chunk's products go by groups of GS token operands, the first half of
+    // k first, each read from LDS while the group before is multiplied
+    constexpr int GS = MT % 4 == 0 ? 4 : MT == 10 ? 5 : MT == 6 ? 3 : MT, NG = 2 * MT / GS;
+    static_assert(MT % GS == 0, "whole groups");
+    v4i x[2][GS];
+    auto read = [&](int c, int g) {
+      const int h = g / (MT / GS), j0 = g % (MT / GS) * GS;
+      const unsigned char *buf = ring + (c % (D + 1)) * XB + li * SB + 16 * ((4 * h + lg) ^ key(li));
+#pragma unroll
+      for (int j = 0; j < GS; ++j) x[g & 1][j] = *reinterpret_cast<const v4i *>(buf + 16 * (j0 + j) * SB);
+    };
+    auto mul = [&](const v4i (*v)[2], int g) {
+      const int h = g / (MT / GS), j0 = g % (MT / GS) * GS;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < GS; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i][j0 + j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[h][i], x[g & 1][j], acc[i][j0 + j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // Step c multiplies chunk c, whose first group has been read.  Before its
+    // last group, a barrier: chunk c + 1's codes have landed for every wave,
+    // and every wave has read chunk c's, whose place the codes D + 1 chunks
+    // ahead take.  (The loop of whole chunks is entered from straight code:
+    // with a branch on the way the compiler would not know how many loads are
+    // in flight behind the weights it waits for, and wait for all.)
+    int c = 0;
+    if (full >= 2 * D + 1) {
+      issue(0);
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        issue(u + 1);
+        load(w[u], u);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      stage_barrier<D *(LX + LW)>();
+      read(0, 0);
+      do {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+#pragma unroll
+          for (int g = 0; g < NG - 1; ++g) {
+            read(c + u, g + 1);
+            mul(w[u], g);
+          }
+          stage_barrier<(D - 1) * (LX + LW) + LW>();
+          read(c + u + 1, 0);
+          issue(c + u + 1 + D);
+          mul(w[u], NG - 1);
+          load(w[u], c + u + D);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        c += D;
+      } while (c + 2 * D + 1 <= full);
+    } else {
+#pragma unroll
+      for (int u = 0; u <= D; ++u)
+        if (u < chunks) {
+          issue(u);
+          if (u < D) {
+            if (u < full) load(w[u], u);
+            else load_part(w[u], u);
+          }
+        }
+      stage_barrier<0>();
+      read(0, 0);
+    }
+    for (; c < chunks; c += D) {
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+        if (c + u < chunks) {
+#pragma unroll
+          for (int g = 0; g < NG - 1; ++g) {
+            read(c + u, g + 1);
+            mul(w[u], g);
+          }
+          stage_barrier<0>();
+          if (c + u + 1 < chunks) read(c + u + 1, 0);
+          if (c + u + 1 + D < chunks) issue(c + u + 1 + D);
+          mul(w[u], NG - 1);
+          if (c + u + D < full) load(w[u], c + u + D);
+          else if (c + u + D < chunks) load_part(w[u], c + u + D);
+        }
+    }
+    finish_sweep<MT>(acc, wave, n0);
+  }
+
+  // y, 16 tokens at a time: the waves put their channels side by side in LDS
+  // (8-byte or 16-byte pieces, swizzled by the token), and whole rows of BN
+  // channels are written.
+  template <int MT>
+  __device__ __forceinline__ void finish_sweep(const v4i (*acc)[MT], int wave, int n0) {
+    constexpr int EPC = 16 / (int)sizeof(T);   // elements of a 16-byte chunk
+    constexpr int CH = ROWB / 16;              // chunks of a row
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    const float *ws = a.ws + (size_t)t.e * a.N;
+    float sn[2][4], bn[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = min(n0 + 32 * wave + 16 * i + 4 * lg + r, a.N - 1);
+        sn[i][r] = ws[n];
+        bn[i][r] = a.bias ? a.bias[n] : 0.f;
+      }
+    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (uint64_t)a.ldy * sizeof(T) % 16 == 0;
+    T *y = static_cast<T *>(a.y);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if (16 * j >= t.n) break;
+      const int tt = min(16 * j + li, t.n - 1);
+      const float st = a.s[GROUPED ? in_row<GROUPED>(a, rows[tt]) : t.r0 + tt];
+      stage_barrier<0>();  // the last operands, or the rows before, have been read
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        Pack<T, 4> v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(acc[i][j][r], st, sn[i][r], bn[i][r]);
+        const int e = 32 * wave + 16 * i + 4 * lg;
+        *reinterpret_cast<Pack<T, 4> *>(ring + li * ROWB + (((e / EPC) ^ (li & 7)) * 16) +
+                                        (e % EPC) * (int)sizeof(T)) = v;
+      }
+      stage_barrier<0>();
+      if (vec) {
+        for (int q = threadIdx.x; q < 16 * CH; q += 64 * NW) {
+          const int rr = q / CH, ch = q % CH, n = n0 + ch * EPC;
+          if (16 * j + rr >= t.n || n >= a.N) continue;
+          const int row = GROUPED ? rows[16 * j + rr] : t.r0 + 16 * j + rr;
+          if (row < 0) continue;
+          const Pack<T, EPC> v = *reinterpret_cast<const Pack<T, EPC> *>(ring + rr * ROWB + ((ch ^ (rr & 7)) * 16));
+          T *d = y + (int64_t)row * a.ldy + n;
+          if (n + EPC <= a.N) {
+            *reinterpret_cast<Pack<T, EPC> *>(d) = v;
+          } else {
+#pragma unroll
+            for (int k = 0; k < EPC - 1; ++k)
+              if (n + k < a.N) d[k] = v.v[k];
+          }
+        }
+      } else {
+        for (int q = threadIdx.x; q < 16 * BN; q += 64 * NW) {
+          const int rr = q / BN, k = q % BN;
+          if (16 * j + rr >= t.n || n0 + k >= a.N) continue;
+          const int row = GROUPED ? rows[16 * j + rr] : t.r0 + 16 * j + rr;
+          if (row < 0) continue;
+          y[(int64_t)row * a.ldy + n0 + k] = *reinterpret_cast<const T *>(
+              ring + rr * ROWB + (((k / EPC) ^ (rr & 7)) * 16) + (k % EPC) * (int)sizeof(T));
+        }
+      }
+    }
+  }
+};
+
+// The smallest of the variants MT = 1, 2, 4, 6, ... MAX that holds n tokens.
+template <int MAX, int M = 1, typename K>
+__device__ __forceinline__ void sweep_dispatch(K &k, int n) {
+  if constexpr (M >= MAX) {
+    k.template run<MAX>();
+  } else {
+    if (n <= 16 * M) k.template run<M>();
+    else sweep_dispatch<MAX, M == 1 ? 2 : M + 2>(k, n);
+  }
+}
+
+template <int DT, int BM, int NW, int D, bool GROUPED>
+__global__ __launch_bounds__(64 * NW) void k_q8_sweep(Q8Args a, int nbm, int nbn) {
+  typedef SweepKernel<DT, BM, NW, D, GROUPED> K;
+  __shared__ __align__(16) unsigned char ring[K::LDS];
+  __shared__ int rows[GROUPED ? BM : 1];
+  Tile t;
+  if constexpr (GROUPED) {
+    t = expert_tile<BM>(a, nbn);
+    if (t.n <= 0) return;
+    for (int i = threadIdx.x; i < t.n; i += 64 * NW) rows[i] = out_row<GROUPED>(a, t.r0 + i);
+    __syncthreads();
+  } else {
+    const int id = xcd_item(blockIdx.x, nbm * nbn);
+    if (id < 0) return;
+    const int m = id % nbm;
+    t = Tile{0, m * BM, min(BM, a.rows - m * BM), id / nbm};
+  }
+  K k{a, t, ring, rows};
+  sweep_dispatch<BM / 16>(k, t.n);
+}
+
+// ---------------------------------------------------------------------------
 // Many tokens.  A workgroup of WM x WN waves takes up to BM tokens and BN
 // channels in 32 x 32 products: wave (wm, wn) the token groups of 32 wm, wm +
 // WM, ... and BN / WN consecutive channels.  A tile with fewer tokens (an
@@ -597,34 +879,32 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, uns
 }
 
 template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_q8_tile(Q8Args a, int nbm, int nbn) {
+// (LDS past half a CU's leaves room for one workgroup)
+__global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 : 1) void k_q8_tile(Q8Args a, int nbm, int nbn) {
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
   tile_body<DT, BM, BN, WM, WN, SB, LDS, GROUPED>(a, nbm, nbn, ring, rows);
 }
 
-// Upper bound of the token tiles of BM over E experts with P pairs.
-int64_t max_tiles(const Q8Args &a, int bm) { return a.P / bm + (a.P < a.E ? a.P : a.E); }
-
-// The variants, by the tokens (for each expert, on average) that share a
-// weight row: few tokens stream the weights, more take tiles that are as
-// large as still leave enough of them.
-enum Variant { kRing16, kRing32, kRing64, kRing64Wide, kTile128, kTile256 };
-struct Shape {
-  int bm, bn, threads;
+// ---------------------------------------------------------------------------
+// The variants and the choice among them.  A variant's tile (bm tokens x bn
+// channels) and threads are its kernel's; `slots` is how many of its
+// workgroups the 256 CUs hold at once.
+// ---------------------------------------------------------------------------
+enum Variant {
+  kRing16x16, kRing16x32, kRing32x32, kRing32x64, kRing64x32, kRing64x32Deep, kRing64x64,
+  kSweep32, kSweep64, kTile128, kTile128Deep, kTile256, kVariants
 };
-constexpr Shape kShapes[] = {{16, 32, 256},  {32, 64, 256},   {64, 32, 512},
-                             {64, 128, 512}, {128, 128, 256}, {256, 256, 512}};
+struct Shape {
+  int bm, bn, threads, slots;
+};
+constexpr Shape kShapes[kVariants] = {
+    {16, 16, 256, 512},   {16, 32, 256, 512},  {32, 32, 256, 512},   {32, 64, 256, 512},
+    {64, 32, 512, 512},   {64, 32, 512, 256},  {64, 64, 512, 512},   {32, 64, 128, 2048},
+    {64, 128, 256, 1024}, {128, 128, 256, 512}, {128, 128, 256, 256}, {256, 256, 512, 256}};
 
-Variant variant_of(const Q8Args &a) {
-  const int64_t avg = a.offs ? ((int64_t)a.P + a.E - 1) / a.E : a.rows;
-  if (avg <= (a.offs ? 12 : 16)) return kRing16;
-  if (avg <= (a.offs ? 24 : 32)) return kRing32;
-  if (avg <= (a.offs ? 56 : 64)) return a.offs ? kRing64Wide : kRing64;
-  if (a.offs) return kTile256;
-  if (avg < 1024) return kTile128;
-  return kTile256;
-}
+// Upper bound of the token tiles of bm over E experts with P pairs.
+int64_t max_tiles(const Q8Args &a, int bm) { return a.P / bm + (a.P < a.E ? a.P : a.E); }
 
 int64_t workgroups(const Q8Args &a, Variant v) {
   const Shape &s = kShapes[v];
@@ -633,31 +913,79 @@ int64_t workgroups(const Q8Args &a, Variant v) {
   return (nbm * nbn + 7) / 8 * 8;
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, int GSTAGES>
-void run_ring(const Q8Args &a, int64_t wgs, hipStream_t st) {
-  const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
-  constexpr int NT = 64 * WM * WN * KS;
-  if (a.offs)
-    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, GSTAGES, true>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
-  else
-    hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, false>), dim3(wgs), dim3(NT), 0, st, a, nbm, nbn);
+// Experts' products, by the tokens of an expert on average.  The sweep reads
+// each weight once at the rate of the memory as long as its workgroups fill
+// the chip; the rings split k and fill it with fewer channels.  64 experts of
+// 6144 x 2048: 10 tokens each 148 us by kSweep32 (ring 163), 31 tokens 165 us
+// by kSweep64 (ring 208); 256 experts of 4096 x 6144: 64 tokens 1370 us by
+// kTile256 (a sweep of up to 192 tokens 1436), 128 tokens 1534 (1613).
+Variant grouped_variant(const Q8Args &a) {
+  const int64_t avg = ((int64_t)a.P + a.E - 1) / a.E;
+  const int64_t used = a.P < a.E ? a.P : a.E;  // experts with a token, at most
+  if (avg <= 12) return used * (a.N / 64) >= 1024 ? kSweep32 : kRing16x32;
+  if (avg <= 52) return used * (a.N / 128) >= 512 ? kSweep64 : kRing64x32;
+  return kTile256;
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS>
+// The dense product.  Up to 64 tokens one token tile reads the weights, and
+// the narrower blocks are taken while they leave CUs without a workgroup
+// (6144 columns: 1 token x 2048 channels 5.3 us by 16 x 16 against 5.8 by 16 x
+// 32, 6144 channels 8.1 against 7.5; 61 tokens x 131072 channels 160 us by
+// kSweep64 against 177 by 64 x 64).  More tokens: the least time as measured
+// at 6144 columns, a kernel's time with at most one workgroup a CU or that of
+// a full round of its slots (512 x 6144: kTile128Deep 34 us, 64 x 64 41;
+// 1024: kTile128 50, 64 x 64 68, kTile256 75; 2048: kTile256 85, kTile128 91;
+// 200: 64 x 64 22, kTile128Deep 31).
+Variant dense_variant(const Q8Args &a) {
+  if (a.rows <= 16) return a.N <= 4096 ? kRing16x16 : kRing16x32;
+  if (a.rows <= 32) return a.N <= 8192 ? kRing32x32 : kRing32x64;
+  if (a.rows <= 64)
+    return a.N <= 8192 ? kRing64x32Deep : a.N >= 65536 ? kSweep64 : kRing64x32;
+  struct Time {
+    Variant v;
+    int first, round;
+  };
+  constexpr Time kTimes[] = {{kRing64x32, 11, 17}, {kRing64x64, 19, 25}, {kTile128Deep, 31, 1000},
+                             {kTile128, 35, 50},   {kTile256, 72, 86}};
+  Variant best = kTile256;
+  int64_t least = INT64_MAX;
+  for (const Time &t : kTimes) {
+    const int64_t n = workgroups(a, t.v), slots = kShapes[t.v].slots;
+    const int64_t cost = n <= 256 ? t.first : t.round * ((n + slots - 1) / slots);
+    if (cost < least) {
+      least = cost;
+      best = t.v;
+    }
+  }
+  return best;
+}
+
+Variant variant_of(const Q8Args &a) { return a.offs ? grouped_variant(a) : dense_variant(a); }
+
+template <int DT, bool GROUPED, int BM, int BN, int WM, int WN, int KS, int STAGES>
+void run_ring(const Q8Args &a, int64_t wgs, hipStream_t st) {
+  const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
+  hipLaunchKernelGGL((k_q8_ring<DT, BM, BN, WM, WN, KS, STAGES, GROUPED>), dim3(wgs),
+                     dim3(64 * WM * WN * KS), 0, st, a, nbm, nbn);
+}
+
+template <int DT, bool GROUPED, int BM, int NW, int D>
+void run_sweep(const Q8Args &a, int64_t wgs, hipStream_t st) {
+  const int nbn = (a.N + 32 * NW - 1) / (32 * NW), nbm = (a.rows + BM - 1) / BM;
+  hipLaunchKernelGGL((k_q8_sweep<DT, BM, NW, D, GROUPED>), dim3(wgs), dim3(64 * NW), 0, st, a, nbm, nbn);
+}
+
+template <int DT, bool GROUPED, int BM, int BN, int WM, int WN, int SB, int LDS>
 void run_tile(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
-  if (a.offs)
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, true>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
-                       nbm, nbn);
-  else
-    hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, false>), dim3(wgs), dim3(64 * WM * WN), 0, st, a,
-                       nbm, nbn);
+  hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, GROUPED>), dim3(wgs), dim3(64 * WM * WN), 0, st,
+                     a, nbm, nbn);
 }
 
 }  // namespace
 
 bool gemm_q8_fits(const Q8Args &a) {
-  // (the grouped tiles name rows of q by 32-bit byte offsets)
+  // (the grouped kernels name rows of q by 32-bit byte offsets)
   if (a.offs && (int64_t)a.rows * a.K >= (int64_t)1 << 32) return false;
   const Variant v = variant_of(a);
   return workgroups(a, v) * kShapes[v].threads < ((int64_t)1 << 31);
@@ -669,13 +997,28 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
   const int64_t wgs = workgroups(a, v);
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
-    switch (v) {
-      case kRing16: run_ring<DT, 16, 32, 1, 1, 4, 6, 3>(a, wgs, st); break;
-      case kRing32: run_ring<DT, 32, 64, 1, 1, 4, 3, 3>(a, wgs, st); break;
-      case kRing64: run_ring<DT, 64, 32, 2, 1, 4, 6, 3>(a, wgs, st); break;
-      case kRing64Wide: run_ring<DT, 64, 128, 2, 2, 2, 3, 3>(a, wgs, st); break;
-      case kTile128: run_tile<DT, 128, 128, 2, 2, 128, 64 << 10>(a, wgs, st); break;
-      case kTile256: run_tile<DT, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
+    if (a.offs) {
+      switch (v) {
+        case kRing16x32: run_ring<DT, true, 16, 32, 1, 1, 4, 3>(a, wgs, st); break;
+        case kRing64x32: run_ring<DT, true, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
+        case kSweep32: run_sweep<DT, true, 32, 2, 4>(a, wgs, st); break;
+        case kSweep64: run_sweep<DT, true, 64, 4, 3>(a, wgs, st); break;
+        default: run_tile<DT, true, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
+      }
+    } else {
+      switch (v) {
+        case kRing16x16: run_ring<DT, false, 16, 16, 1, 1, 4, 8>(a, wgs, st); break;
+        case kRing16x32: run_ring<DT, false, 16, 32, 1, 1, 4, 6>(a, wgs, st); break;
+        case kRing32x32: run_ring<DT, false, 32, 32, 1, 1, 4, 4>(a, wgs, st); break;
+        case kRing32x64: run_ring<DT, false, 32, 64, 1, 1, 4, 3>(a, wgs, st); break;
+        case kRing64x32: run_ring<DT, false, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
+        case kRing64x32Deep: run_ring<DT, false, 64, 32, 2, 1, 4, 6>(a, wgs, st); break;
+        case kRing64x64: run_ring<DT, false, 64, 64, 2, 2, 2, 2>(a, wgs, st); break;
+        case kSweep64: run_sweep<DT, false, 64, 4, 3>(a, wgs, st); break;
+        case kTile128: run_tile<DT, false, 128, 128, 2, 2, 128, 64 << 10>(a, wgs, st); break;
+        case kTile128Deep: run_tile<DT, false, 128, 128, 2, 2, 128, 128 << 10>(a, wgs, st); break;
+        default: run_tile<DT, false, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
+      }
     }
     return hipGetLastError();
   });

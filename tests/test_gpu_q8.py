@@ -155,7 +155,13 @@ def test_swiglu_far_values():
     (1, 1, 32), (1, 17, 96), (2, 16, 128), (5, 100, 160), (12, 33, 1024), (13, 64, 6144),
     (16, 31, 2080), (28, 48, 224), (29, 70, 352), (64, 96, 544), (65, 130, 160), (127, 257, 96),
     (128, 128, 128), (129, 127, 2048), (300, 200, 32), (515, 259, 288), (1024, 256, 64),
-    (1500, 515, 416), (1, 2048, 6144), (3, 300, 8192), (1, 5, 131040), (70, 40, 16416)])
+    (1500, 515, 416), (1, 2048, 6144), (3, 300, 8192), (1, 5, 131040), (70, 40, 16416),
+    # sizes from which other variants are taken: blocks of 32 and 64 channels,
+    # the sweep (whole and part chunks, few and many), 64 x 64, the tiles
+    (3, 4100, 288), (16, 4097, 2592), (20, 8200, 96), (31, 8193, 1568), (61, 8200, 544),
+    (61, 65601, 32), (33, 65536, 896), (64, 65550, 1120), (200, 6145, 800), (512, 6144, 160),
+    (509, 6147, 544), (1024, 6145, 96), (1021, 6144, 416), (2048, 6150, 160), (2047, 6144, 608),
+    (2048, 6144, 32), (2100, 6145, 1056)])
 @pytest.mark.parametrize("dt,bias", [("f32", False), ("bf16", True), ("f16", False)])
 def test_gemm_q8(T, N, K, dt, bias):
     q, w = codes(T, K, seed=1), codes(N, K, seed=2)
@@ -221,7 +227,12 @@ def routing(T, k, E, seed, drop=0.0, few=None):
     (1, 1, 1, 5, 32, 0, None), (1, 8, 256, 48, 96, 0, None), (3, 8, 256, 33, 544, 0.3, None),
     (40, 2, 5, 70, 160, 0.5, None), (7, 3, 100, 16, 128, 0, 3), (200, 4, 9, 40, 224, 0.2, None),
     (600, 2, 8, 140, 96, 0.1, None), (300, 2, 2, 130, 64, 0, None), (1500, 2, 3, 260, 160, 0.2, None),
-    (65, 1, 1024, 20, 64, 0, None), (33, 2, 1000, 30, 32, 0, 2), (5, 2, 7, 30, 64, 1.0, None)])
+    (65, 1, 1024, 20, 64, 0, None), (33, 2, 1000, 30, 32, 0, 2), (5, 2, 7, 30, 64, 1.0, None),
+    # the sweeps (up to 32 and 64 tokens a tile; whole and part chunks, few and
+    # many), experts with more tokens than a tile, one expert with all of them
+    (40, 8, 64, 1100, 96, 0.1, None), (33, 8, 64, 1089, 1216, 0, None), (64, 8, 300, 260, 1184, 0, None),
+    (160, 8, 64, 1100, 64, 0.1, None), (161, 8, 64, 1101, 1024, 0.1, None), (330, 8, 64, 1090, 1248, 0, None),
+    (300, 4, 40, 1700, 928, 0, 4), (24, 4, 40, 1700, 608, 0, 4), (700, 1, 9, 600, 96, 0, 1)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("fan", [True, False])
 def test_gemm_q8_grouped(T, k, E, N, K, drop, few, dt, fan):
