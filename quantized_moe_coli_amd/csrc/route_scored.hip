@@ -16,6 +16,7 @@
 // rounding to binary32 needs.
 #include <cmath>
 
+#include "exp64.hpp"
 #include "q8.hpp"
 
 #pragma clang fp contract(off)
@@ -24,37 +25,6 @@ namespace coli {
 namespace {
 
 constexpr float kOff = -INFINITY;  // score of an expert that cannot be chosen
-
-// exp(x) in binary64: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor
-// series of e^r up to r^11 (the rest is below 2^-47 of the result).  Past
-// +-1100 it is 0 or infinity, whatever x.
-__device__ __forceinline__ double exp_64(double x) {
-  x = __builtin_fmin(__builtin_fmax(x, -1100.0), 1100.0);
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
-  r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);
-  double p = 1.0 / 39916800;
-  p = __builtin_fma(p, r, 1.0 / 3628800);
-  p = __builtin_fma(p, r, 1.0 / 362880);
-  p = __builtin_fma(p, r, 1.0 / 40320);
-  p = __builtin_fma(p, r, 1.0 / 5040);
-  p = __builtin_fma(p, r, 1.0 / 720);
-  p = __builtin_fma(p, r, 1.0 / 120);
-  p = __builtin_fma(p, r, 1.0 / 24);
-  p = __builtin_fma(p, r, 1.0 / 6);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)n);
-}
-
-// 1 / x for x >= 1, to about 2^-50; 0 for an infinity.
-__device__ __forceinline__ double inverse_64(double x) {
-  double y = __builtin_amdgcn_rcp(x);
-  if (x > 1e300) return y;
-  y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
-  return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
-}
 
 // The two largest of (b1 >= b2) and the partner's, by one move of the lanes.
 template <int CTRL>
@@ -202,6 +172,154 @@ __device__ __forceinline__ void route_token(const ScoreCfg &c, const typename El
   }
 }
 
+// ---------------------------------------------------------------------------
+// Four tokens a wave, 16 lanes each: a step of a reduction, a round of the
+// selection and a ballot then serve four tokens at once.  For batches that
+// fill the chip; a token alone takes longer than by a wave of its own.
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float row_max_step(float v) { return fmaxf(v, dpp_f32<CTRL>(v)); }
+
+// The largest value of the 16 lanes, in all of them (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float row_max(float v) {
+  v = row_max_step<0x128>(v);
+  v = row_max_step<0x124>(v);
+  v = row_max_step<0x122>(v);
+  return row_max_step<0x121>(v);
+}
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, dpp_i32<0x128>(v));
+  v = min(v, dpp_i32<0x124>(v));
+  v = min(v, dpp_i32<0x122>(v));
+  return min(v, dpp_i32<0x121>(v));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += dpp_f64<0x128>(v);
+  v += dpp_f64<0x124>(v);
+  v += dpp_f64<0x122>(v);
+  return v + dpp_f64<0x121>(v);
+}
+
+constexpr int kRowLanes = 16, kRowK = 16;  // lanes of a token, experts at most
+
+// L lanes of the 16 for each group.
+template <int DT, int EPL>
+__global__ __launch_bounds__(256) void k_route_rows(
+    ScoreCfg c, const typename Elem<DT>::type *__restrict__ logits, int64_t ld,
+    const float *__restrict__ bias, int T, int L, int32_t *__restrict__ idx_out,
+    float *__restrict__ w_out) {
+  __shared__ float chosen[256 / kRowLanes][kRowK];
+  const int lane = threadIdx.x & 15, slot = threadIdx.x / kRowLanes;
+  const int t = blockIdx.x * (256 / kRowLanes) + slot;
+  const bool real = t < T;  // (the lanes of no token run along: the moves need all of them)
+  const auto *row = logits + (int64_t)(real ? t : 0) * ld;
+  const int per = c.E / c.n_group;
+  const int g = lane / L, l = lane % L;
+
+  float p[EPL], s[EPL];
+  {
+    float lg[EPL], b[EPL];
+#pragma unroll
+    for (int m = 0; m < EPL; ++m) {
+      const int i = l + m * L;
+      const bool in = g < c.n_group && i < per;
+      const int e = in ? g * per + i : 0;
+      const float v = (float)row[e];
+      b[m] = bias ? bias[e] : 0.f;
+      lg[m] = in && v > kOff ? v : kOff;  // NaN: off
+    }
+    if (c.score == COLI_SCORE_SOFTMAX) {
+      float top = lg[0];
+#pragma unroll
+      for (int m = 1; m < EPL; ++m) top = fmaxf(top, lg[m]);
+      top = row_max(top);
+      double e[EPL], sum = 0.0;
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) {
+        e[m] = lg[m] == top ? 1.0 : exp_64((double)lg[m] - (double)top);
+        if (lg[m] == kOff) e[m] = 0.0;
+        sum += e[m];
+      }
+      sum = row_sum(sum);
+      const double inv = sum >= 1.0 ? inverse_64(sum) : 0.0;
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) p[m] = (float)(e[m] * inv);
+    } else {
+#pragma unroll
+      for (int m = 0; m < EPL; ++m)
+        p[m] = lg[m] == kOff ? 0.f : (float)inverse_64(1.0 + exp_64(-(double)lg[m]));
+    }
+#pragma unroll
+    for (int m = 0; m < EPL; ++m) {
+      const float v = bias ? p[m] + b[m] : p[m];
+      s[m] = lg[m] > kOff && v > kOff ? v : kOff;
+    }
+  }
+
+  if (c.topk_group < c.n_group) {
+    float b1 = kOff, b2 = kOff;  // the group's two best
+#pragma unroll
+    for (int m = 0; m < EPL; ++m) {
+      b2 = fmaxf(b2, fminf(b1, s[m]));
+      b1 = fmaxf(b1, s[m]);
+    }
+    if (L >= 2) top2_step<0xB1>(b1, b2);
+    if (L >= 4) top2_step<0x4E>(b1, b2);
+    if (L >= 8) top2_step<0x141>(b1, b2);
+    const float gs = c.group_score == COLI_GROUP_TOP2 && b2 > kOff ? b1 + b2 : b1;
+    int ahead = 0;
+    for (int o = 0; o < c.n_group; ++o) {
+      const float v = __shfl(gs, o * L, kRowLanes);
+      ahead += v > gs || (v == gs && o < g);
+    }
+    if (ahead >= c.topk_group) {
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) s[m] = kOff;
+    }
+  }
+
+  int my_idx = -1;
+  float best = kOff, bp = 0.f;
+  int bm = 0;
+  auto local_best = [&] {
+    best = s[0], bp = p[0], bm = 0;
+#pragma unroll
+    for (int m = 1; m < EPL; ++m) {
+      const bool more = s[m] > best;
+      best = more ? s[m] : best;
+      bp = more ? p[m] : bp;
+      bm = more ? m : bm;
+    }
+  };
+  local_best();
+  for (int j = 0; j < c.k; ++j) {
+    const float wb = row_max(best);
+    const int at = g * per + l + bm * L;
+    const int wi = row_min(best == wb ? at : 0x7fffffff);
+    const bool any = wb > kOff;
+    if (lane == j && any) my_idx = wi;
+    if (any && best == wb && at == wi) {
+      chosen[slot][j] = bp;
+#pragma unroll
+      for (int m = 0; m < EPL; ++m) s[m] = m == bm ? kOff : s[m];
+    } else if (!any && lane == j) {
+      chosen[slot][j] = 0.f;
+    }
+    local_best();
+  }
+  __syncthreads();
+  if (real && lane < c.k) {
+    float w = chosen[slot][lane];
+    if (c.norm) {
+      float total = 0.f;
+      for (int j = 0; j < c.k; ++j) total += chosen[slot][j];
+      w = total > 0.f ? w / total : 0.f;
+    }
+    idx_out[(int64_t)t * c.k + lane] = my_idx;
+    w_out[(int64_t)t * c.k + lane] = my_idx < 0 ? 0.f : w * c.rsf;
+  }
+}
+
 constexpr int kRouteWaves = 4;  // tokens of a workgroup
 
 template <int DT, int EPL>
@@ -224,9 +342,24 @@ hipError_t launch_route_scored(int dt, const ScoreCfg &c, const void *logits, in
   while (gp < c.n_group) gp *= 2;
   const int L = 64 / gp;
   const int need = (c.E / c.n_group + L - 1) / L;  // at most 32: E <= 1024, gp < 2 n_group
+  // four tokens a wave from 1024 tokens on (16384 x 256: 17.8 us, by a wave each 23.4), where 16 lanes
+  // hold a token's experts in 16 registers each
+  const int L16 = gp <= kRowLanes ? kRowLanes / gp : 0;
+  const int need16 = L16 ? (c.E / c.n_group + L16 - 1) / L16 : 99;
+  const bool rows = T >= 1024 && need16 <= 16 && c.k <= kRowK;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     const auto *lg = static_cast<const typename Elem<DT>::type *>(logits);
+    if (rows) {
+      auto by16 = [&](auto epl) {
+        hipLaunchKernelGGL((k_route_rows<DT, decltype(epl)::value>), dim3((T + 15) / 16), dim3(256), 0, st, c,
+                           lg, ld, bias, T, L16, idx, w);
+      };
+      if (need16 <= 4) by16(std::integral_constant<int, 4>());
+      else if (need16 <= 8) by16(std::integral_constant<int, 8>());
+      else by16(std::integral_constant<int, 16>());
+      return hipGetLastError();
+    }
     auto go = [&](auto epl) {
       hipLaunchKernelGGL((k_route_scored<DT, decltype(epl)::value>), dim3((T + kRouteWaves - 1) / kRouteWaves),
                          dim3(64 * kRouteWaves), 0, st, c, lg, ld, bias, T, L, idx, w);

@@ -389,6 +389,26 @@ def test_route_scored_ties_masks_and_infinities(score, gs):
     check_route(torch.randn(4, E, generator=gen(5)), bias, (E, k, G, TG, score, gs, True, 1.0))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("score,gs", [("softmax", "max"), ("sigmoid", "top2")])
+@pytest.mark.parametrize("T,E,k,G,TG", [(1024, 256, 8, 1, 1), (1029, 256, 8, 8, 4), (1500, 60, 6, 4, 2),
+                                        (1025, 16, 9, 16, 9), (1031, 7, 3, 1, 1), (1030, 128, 4, 2, 1),
+                                        (1027, 256, 17, 1, 1), (1026, 45, 5, 9, 3), (1033, 512, 8, 8, 3)])
+def test_route_scored_batches(dt, score, gs, T, E, k, G, TG):
+    """Batches that take the four-tokens-a-wave kernel, and neighbours of its
+    limits; with ties, dead experts and rows without any."""
+    g = gen(T, E, k)
+    logits = (torch.randn(T, E, generator=g) * 2)
+    logits[::3] = torch.randint(-3, 4, (len(range(0, T, 3)), E), generator=g).float()
+    logits[torch.rand(T, E, generator=g) < 0.1] = float("-inf")
+    logits[5] = float("-inf")
+    logits[7] = float("nan")
+    logits[9, : E // 2] = float("inf")
+    logits[11] = torch.finfo(torch.bfloat16).min
+    bias = torch.randn(E, generator=g) * 0.02 if E % 2 else None
+    check_route(logits, bias, (E, k, G, TG, score, gs, T % 2 == 0, 2.5), dt)
+
+
 def test_route_scored_strided_rows_and_matches_sigmoid_router():
     """Rows of a wider buffer; and with sigmoid scores, groups by their two
     best and normalised weights it is coli_moe_route, bit for bit."""
