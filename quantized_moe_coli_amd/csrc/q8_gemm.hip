@@ -217,6 +217,27 @@ struct RingKernel {
                                          (lds_void *)(buf + (i * NW + wave) * 1024), 16, 0, 0);
     };
 
+    // The scales and biases of the 16 x 16 results this wave will finish, so
+    // that nothing is waited for after the last product: lane (li, lg) has
+    // token li and channels 4 lg .. of each.
+    constexpr int TILES = (BM / 16) * (BN / 16), TPW = (TILES + NW - 1) / NW;
+    float st[TPW], sn[TPW][4], bn[TPW][4];
+    int orow[TPW];  // -1: none
+#pragma unroll
+    for (int q = 0; q < TPW; ++q) {
+      const int tl = min(q * NW + wave, TILES - 1);
+      const int tt = min((tl / (BN / 16)) * 16 + li, t.n - 1), n = n0 + (tl % (BN / 16)) * 16 + 4 * lg;
+      orow[q] = GROUPED ? rows[tt] : t.r0 + tt;
+      st[q] = a.s[in_row<GROUPED>(a, orow[q])];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int nr = min(n + r, a.N - 1);
+        sn[q][r] = a.ws[(size_t)t.e * a.N + nr];
+        bn[q][r] = a.bias ? a.bias[nr] : 0.f;
+      }
+    }
+    asm volatile("" ::: "memory");  // (these loads stay ahead of the stages')
+
     v4i acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
@@ -267,7 +288,6 @@ struct RingKernel {
 
     stage_barrier<0>();
     int *part = reinterpret_cast<int *>(ring);
-    constexpr int TILES = (BM / 16) * (BN / 16);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -276,27 +296,21 @@ struct RingKernel {
         *reinterpret_cast<v4i *>(part + (kq * TILES + tl) * 256 + 4 * lane) = acc[i][j];
       }
     __syncthreads();
-    // lane: token li, channels 4 lg .. of a 16 x 16 product
     T *y = static_cast<T *>(a.y);
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(T)) == 0 && a.ldy % 4 == 0;
-    for (int tl = wave; tl < TILES; tl += NW) {
+#pragma unroll
+    for (int q = 0; q < TPW; ++q) {
+      const int tl = q * NW + wave;
       const int tt = (tl / (BN / 16)) * 16 + li, n = n0 + (tl % (BN / 16)) * 16 + 4 * lg;
-      if (tt >= t.n || n >= a.N) continue;
-      const int row = GROUPED ? rows[tt] : t.r0 + tt;
-      if (row < 0) continue;
+      if (tl >= TILES || tt >= t.n || n >= a.N || orow[q] < 0) continue;
       v4i sum = *reinterpret_cast<const v4i *>(part + tl * 256 + 4 * lane);
 #pragma unroll
       for (int k = 1; k < KS; ++k)
         sum += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
-      const float st = a.s[in_row<GROUPED>(a, row)];
-      const float *ws = a.ws + (size_t)t.e * a.N;
       Pack<T, 4> v;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int nr = min(n + r, a.N - 1);
-        v.v[r] = (T)finish(sum[r], st, ws[nr], a.bias ? a.bias[nr] : 0.f);
-      }
-      T *d = y + (int64_t)row * a.ldy + n;
+      for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(sum[r], st[q], sn[q][r], bn[q][r]);
+      T *d = y + (int64_t)orow[q] * a.ldy + n;
       if (vec && n + 4 <= a.N) {
         *reinterpret_cast<Pack<T, 4> *>(d) = v;
       } else {
@@ -777,9 +791,10 @@ struct TileKernel {
   // store writes whole runs of a row.
   template <int TMV>
   __device__ __forceinline__ void finish_tile(const v16i (*acc)[TMV], int wave, int wm, int wn, int n0) {
-    constexpr int ROWB = 32 * TN * (int)sizeof(T);  // bytes of a row in the area
-    constexpr int CH = ROWB / 16;                   // 16-byte chunks in it
-    constexpr int EPC = 16 / (int)sizeof(T);        // elements of a chunk
+    constexpr int EPC = 16 / (int)sizeof(T);        // elements of a 16-byte chunk
+    constexpr int CH = 32 * TN / EPC;               // chunks of a row
+    // bytes of a row in the area: chunk c of row r lies at c ^ (r % 8)
+    constexpr int ROWB = 16 * (CH <= 8 ? 8 : CH <= 16 ? 16 : 32);
     static_assert(NW * 32 * ROWB <= LDS, "area");
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
@@ -819,7 +834,8 @@ struct TileKernel {
       if (vec) {
 #pragma unroll
         for (int p = 0; p < 32 * CH / 64; ++p) {
-          const int rr = p * (64 / CH) + lane / CH, ch = lane % CH;
+          const int rr = 64 % CH == 0 ? p * (64 / CH) + lane / CH : (p * 64 + lane) / CH;
+          const int ch = 64 % CH == 0 ? lane % CH : (p * 64 + lane) % CH;
           const Pack<T, EPC> v = *reinterpret_cast<const Pack<T, EPC> *>(area + rr * ROWB + ((ch ^ (rr & 7)) * 16));
           const int n = nw + ch * EPC;
           if (t0 + rr >= t.n || n >= a.N) continue;
@@ -852,6 +868,17 @@ struct TileKernel {
   }
 };
 
+// The variant for tm (up to M) token groups of each wave.
+template <int M, typename K>
+__device__ __forceinline__ void tile_dispatch(K &k, int tm) {
+  if constexpr (M == 1) {
+    k.template run<1>();
+  } else {
+    if (tm >= M) k.template run<M>();
+    else tile_dispatch<M - 1>(k, tm);
+  }
+}
+
 template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
 __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows) {
   Tile t;
@@ -870,12 +897,7 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, uns
   for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
   __syncthreads();
   TileKernel<DT, BM, BN, WM, WN, SB, LDS, GROUPED> k{a, t, ring, rows};
-  constexpr int TMAX = BM / WM / 32;
-  const int tm = (t.n + 32 * WM - 1) / (32 * WM);
-  if (TMAX >= 4 && tm >= 4) k.template run<TMAX < 4 ? TMAX : 4>();
-  else if (TMAX >= 3 && tm == 3) k.template run<TMAX < 3 ? TMAX : 3>();
-  else if (TMAX >= 2 && tm == 2) k.template run<TMAX < 2 ? TMAX : 2>();
-  else k.template run<1>();
+  tile_dispatch<BM / WM / 32>(k, (t.n + 32 * WM - 1) / (32 * WM));
 }
 
 template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
@@ -918,7 +940,10 @@ int64_t workgroups(const Q8Args &a, Variant v) {
 // the chip; the rings split k and fill it with fewer channels.  64 experts of
 // 6144 x 2048: 10 tokens each 148 us by kSweep32 (ring 163), 31 tokens 165 us
 // by kSweep64 (ring 208); 256 experts of 4096 x 6144: 64 tokens 1370 us by
-// kTile256 (a sweep of up to 192 tokens 1436), 128 tokens 1534 (1613).
+// kTile256 (a sweep of up to 192 tokens 1436), 128 tokens 1493 (1613).
+// (The experts' kTile256 gives each wave 32 channels of all tokens: cost
+// follows the tokens by 32, and three stages fit up to 160 tokens; by 2 x 4
+// waves as in the dense product 1544 us.)
 Variant grouped_variant(const Q8Args &a) {
   const int64_t avg = ((int64_t)a.P + a.E - 1) / a.E;
   const int64_t used = a.P < a.E ? a.P : a.E;  // experts with a token, at most
@@ -1003,7 +1028,7 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
         case kRing64x32: run_ring<DT, true, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
         case kSweep32: run_sweep<DT, true, 32, 2, 4>(a, wgs, st); break;
         case kSweep64: run_sweep<DT, true, 64, 4, 3>(a, wgs, st); break;
-        default: run_tile<DT, true, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
+        default: run_tile<DT, true, 256, 256, 1, 8, 128, 157 << 10>(a, wgs, st); break;
       }
     } else {
       switch (v) {
