@@ -60,6 +60,14 @@ __device__ __forceinline__ int in_row(const Q8Args &a, int out) {
   else return out;
 }
 
+// Keeps what is before it before what is after it.  The waits below count the
+// loads issued since the one that is waited for, so loads of one stage must
+// not be moved past those of another.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Workgroup b runs on XCD b % 8, each with its own L2: an XCD takes a
 // contiguous run of the `total` items, so that neighbours share it.
 __device__ __forceinline__ int xcd_item(int b, int total) {
@@ -236,7 +244,7 @@ struct RingKernel {
         bn[q][r] = a.bias ? a.bias[nr] : 0.f;
       }
     }
-    asm volatile("" ::: "memory");  // (these loads stay ahead of the stages')
+    keep_order();
 
     v4i acc[TN][TM];
 #pragma unroll
@@ -268,8 +276,10 @@ struct RingKernel {
     };
 
 #pragma unroll
-    for (int c = 0; c < STAGES - 1; ++c)
+    for (int c = 0; c < STAGES - 1; ++c) {
       if (c < stages) issue(c);
+      keep_order();
+    }
     for (int c = 0; c < stages; ++c) {
       // stage c has landed for every wave, and no wave reads stage c - 1 any more
       if (c + STAGES - 1 <= stages) stage_barrier<NL *(STAGES - 2)>();
@@ -466,12 +476,14 @@ struct SweepKernel {
     int c = 0;
     if (full >= 2 * D + 1) {
       issue(0);
+      keep_order();
 #pragma unroll
       for (int u = 0; u < D; ++u) {
         issue(u + 1);
+        keep_order();
         load(w[u], u);
+        keep_order();
       }
-      __builtin_amdgcn_sched_barrier(0);
       stage_barrier<D *(LX + LW)>();
       read(0, 0);
       do {
@@ -486,8 +498,9 @@ struct SweepKernel {
           read(c + u + 1, 0);
           issue(c + u + 1 + D);
           mul(w[u], NG - 1);
+          keep_order();
           load(w[u], c + u + D);
-          __builtin_amdgcn_sched_barrier(0);
+          keep_order();
         }
         c += D;
       } while (c + 2 * D + 1 <= full);
@@ -751,8 +764,10 @@ struct TileKernel {
 
     Ops A, B;
 #pragma unroll
-    for (int c = 0; c < STAGES; ++c)
+    for (int c = 0; c < STAGES; ++c) {
       if (c < stages) issue(c);
+      keep_order();
+    }
     if (stages >= STAGES) stage_barrier<NL *(STAGES - 1)>();
     else stage_barrier<0>();
     read(0, 0, A);
@@ -771,6 +786,7 @@ struct TileKernel {
       else stage_barrier<0>();
       if (c + 1 < stages) read(c + 1, 0, A);
       if (c + STAGES < stages) issue(c + STAGES);
+      keep_order();
       mul(B);
     }
     // the part of a stage that is left (K is a multiple of 32)

@@ -64,7 +64,8 @@ def test_gemm_q8_grouped():
         dict(ws=None), dict(E=0), dict(E=1025), dict(N=0), dict(K=0), dict(K=48), dict(K=131072),
         dict(offs=None), dict(offs=P + 2), dict(perm=None), dict(perm=P + 1), dict(Pn=-1),
         dict(Pn=(1 << 25) + 1), dict(fan=0), dict(fan=-1), dict(dt=7), dict(y=None), dict(ldy=9)])
-    refuse("coli_gemm_q8_grouped", good, [dict(Pn=1 << 25, N=1 << 30, ldy=1 << 30)], UNSUPPORTED)
+    refuse("coli_gemm_q8_grouped", good, [dict(Pn=1 << 25, N=1 << 30, ldy=1 << 30),
+                                          dict(rows=1 << 16, K=1 << 16)], UNSUPPORTED)
     no_device_or_empty("coli_gemm_q8_grouped", good, dict(Pn=0, rows=0))
 
 
