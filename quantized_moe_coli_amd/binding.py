@@ -314,7 +314,7 @@ def _refuse(t, dtype, numel, dev, name):
 
 def _rowed(t, rows, cols, dtype, dev, name):
     """(address, row stride) of a [rows, cols] tensor whose rows are dense."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -343,9 +343,9 @@ def _float_type(t, name):
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -367,7 +367,7 @@ def coli_moe_route_scored(cfg: ScoreCfg, logits: torch.Tensor, bias: torch.Tenso
         ctypes.byref(cfg), dt, lp, ld,
         None if bias is None else _dense(bias, torch.float32, E, dev, "bias"), T,
         _dense(idx, torch.int32, T * k, dev, "idx"), _dense(w, torch.float32, T * k, dev, "w"),
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 def coli_quant_act_token(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
@@ -378,7 +378,7 @@ def coli_quant_act_token(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stre
     xp, ld = _rowed(x, T, n, x.dtype, dev, "x")
     _check("coli_quant_act_token", lib().coli_quant_act_token(
         dt, xp, ld, T, n, _dense(q, torch.int8, T * n, dev, "q"),
-        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream)))
+        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream, dev)))
 
 
 def coli_swiglu_quant_token(g: torch.Tensor, u: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
@@ -392,7 +392,7 @@ def coli_swiglu_quant_token(g: torch.Tensor, u: torch.Tensor, q: torch.Tensor, s
     up, ldu = _rowed(u, T, n, g.dtype, dev, "u")
     _check("coli_swiglu_quant_token", lib().coli_swiglu_quant_token(
         dt, gp, ldg, up, ldu, T, n, _dense(q, torch.int8, T * n, dev, "q"),
-        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream)))
+        _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream, dev)))
 
 
 def coli_gemm_q8(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
@@ -408,7 +408,7 @@ def coli_gemm_q8(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Te
         _dense(q, torch.int8, T * K, dev, "q"), _dense(s, torch.float32, T, dev, "s"), T,
         _dense(w, torch.uint8, N * K, dev, "w"), _dense(ws, torch.float32, N, dev, "ws"), N, K,
         None if bias is None else _dense(bias, torch.float32, N, dev, "bias"), dt, yp, ld,
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 def coli_gemm_q8_grouped(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
@@ -429,7 +429,7 @@ def coli_gemm_q8_grouped(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: 
         _dense(w, torch.uint8, E * N * K, dev, "w"),
         _dense(ws, torch.float32, E * N, dev, "ws"), E, N, K,
         _dense(offs, torch.int32, E + 1, dev, "offs"), _dense(perm, torch.int32, P, dev, "perm"),
-        P, fan, dt, yp, ld, _raw_stream(stream)))
+        P, fan, dt, yp, ld, _raw_stream(stream, dev)))
 
 
 def coli_moe_combine(o: torch.Tensor, idx: torch.Tensor | None, w: torch.Tensor, y: torch.Tensor,
@@ -447,7 +447,7 @@ def coli_moe_combine(o: torch.Tensor, idx: torch.Tensor | None, w: torch.Tensor,
     _check("coli_moe_combine", lib().coli_moe_combine(
         dt, op, ldo, None if idx is None else _dense(idx, torch.int32, T * k, dev, "idx"),
         _dense(w, torch.float32, T * k, dev, "w"), T, k, H, ap, lda, yp, ldy,
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 class MoeLayer:

@@ -11,6 +11,10 @@
 // SwiGLU's h = silu(g) * u is evaluated in binary64 and rounded once to
 // binary32, as the layer's own gate/up kernels do, so that a code next to a
 // rounding border does not depend on how the exponential was approximated.
+//
+// 8192 x 6144 bfloat16 30 us (150 MB, 5.0 TB/s: what a copy reaches); SwiGLU of
+// 32768 x 2048 99 us (335 MB), bound by the binary64 instructions of its
+// exponential; the sum of 4096 x 8 rows of 6144 85 us (453 MB, 5.3 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
