@@ -686,6 +686,7 @@ struct TileKernel {
   const Tile &t;
   unsigned char *ring;   // LDS bytes
   const int *rows;       // [BM] output rows of the tile's tokens (-1: none)
+  const float *chans;    // [BN] the channels' scales
 
   template <int TMV>
   __device__ __forceinline__ void run() {
@@ -826,15 +827,14 @@ struct TileKernel {
     static_assert(NW * 32 * ROWB <= LDS, "area");
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
-    const float *ws = a.ws + (size_t)t.e * a.N;
     float sn[TN][16], bn[TN][16];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int n = min(nw + 32 * i + 8 * (r / 4) + 4 * lh + r % 4, a.N - 1);
-        sn[i][r] = ws[n];
-        bn[i][r] = a.bias ? a.bias[n] : 0.f;
+        const int n = nw + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
+        sn[i][r] = chans[n - n0];
+        bn[i][r] = a.bias ? a.bias[min(n, a.N - 1)] : 0.f;
       }
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && (uint64_t)a.ldy * sizeof(T) % 16 == 0;
     stage_barrier<0>();  // every wave has read its last operands
@@ -844,8 +844,7 @@ struct TileKernel {
     for (int j = 0; j < TMV; ++j) {
       const int t0 = (j * WM + wm) * 32;
       if (t0 >= t.n) break;
-      const int mine = rows[min(t0 + lr, t.n - 1)];
-      const float st = a.s[in_row<GROUPED>(a, mine)];
+      const float st = a.s[in_row<GROUPED>(a, rows[min(t0 + lr, t.n - 1)])];
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -908,7 +907,8 @@ __device__ __forceinline__ void tile_dispatch(K &k, int tm) {
 }
 
 template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
-__device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows) {
+__device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows,
+                                          float *chans) {
   Tile t;
   if constexpr (GROUPED) {
     t = expert_tile<BM>(a, nbn);
@@ -922,9 +922,13 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, uns
     const int m = g * 4 + (id % run) % h;
     t = Tile{0, m * BM, min(BM, a.rows - m * BM), (id % run) / h};
   }
+  // (the channels' scales now, so that the end does not wait for them; the
+  // tokens' too would fill the LDS to its last byte, which costs 13 %)
   for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
+  for (int i = threadIdx.x; i < BN; i += 64 * WM * WN)
+    chans[i] = a.ws[(size_t)t.e * a.N + min(t.nb * BN + i, a.N - 1)];
   __syncthreads();
-  TileKernel<DT, BM, BN, WM, WN, SB, LDS, GROUPED> k{a, t, ring, rows};
+  TileKernel<DT, BM, BN, WM, WN, SB, LDS, GROUPED> k{a, t, ring, rows, chans};
   tile_dispatch<BM / WM / 32>(k, (t.n + 32 * WM - 1) / (32 * WM));
 }
 
@@ -933,7 +937,8 @@ template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 : 1) void k_q8_tile(Q8Args a, int nbm, int nbn) {
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
-  tile_body<DT, BM, BN, WM, WN, SB, LDS, GROUPED>(a, nbm, nbn, ring, rows);
+  __shared__ float chans[BN];
+  tile_body<DT, BM, BN, WM, WN, SB, LDS, GROUPED>(a, nbm, nbn, ring, rows, chans);
 }
 
 // ---------------------------------------------------------------------------
