@@ -150,6 +150,42 @@ def test_swiglu_far_values():
     np.testing.assert_array_equal(q.cpu().numpy(), rq)
 
 
+def test_quant_more_rows_than_one_grid_axis():
+    """Over 2^22 rows of 32: workgroups along both axes.  Every row's codes
+    against the definition in torch, each quotient rounded once from float64
+    (torch divides a float32 tensor by a number by multiplying with 1 / number)."""
+    T, n = (1 << 22) + 5, 32
+    x = torch.randn(T, n, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    q, s = torch.empty(T, n, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    B.coli_swiglu_quant_token(torch.full_like(x, 1e4), x, q, s)  # silu(1e4) = 1e4
+    h = (x.double() * 1e4).float()
+    rs = (h.abs().amax(1).double() / 127).float()
+    assert torch.equal(s, rs)
+    assert torch.equal(q, torch.round((h.double() / rs[:, None].double()).float()).to(torch.int8))
+
+
+def test_calls_on_a_given_stream():
+    """Every call enqueues on the stream it is given, not on the current one."""
+    st = torch.cuda.Stream()
+    T, k, E, H = 4, 2, 4, 64
+    x, q, s = acts(T, H, torch.bfloat16, 1), torch.zeros(T, H, dtype=torch.int8, device="cuda"), torch.zeros(T, device="cuda")
+    w, ws, y = codes(40, H, seed=3), scales(40), torch.zeros(T, 40, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)  # what follows on this stream waits
+    B.coli_quant_act_token(x, q, s, stream=st)
+    B.coli_gemm_q8(q, s, w.view(torch.uint8), ws, y, stream=st)
+    idx, wt = torch.full((T, k), -5, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+    lg = torch.randn(T, E, generator=gen(3)).cuda()
+    early = y.clone()  # on the current stream, which does not wait
+    B.coli_moe_route_scored(B.score_cfg(E, k), lg, None, idx, wt, stream=st.cuda_stream)
+    st.synchronize()
+    assert (early == 0).all()
+    rq, rs = R.quant(f64(x))
+    assert_product(y, R.product(rq, rs, w.cpu().numpy(), ws.cpu().numpy()), torch.float32)
+    assert (idx >= 0).all()
+
+
 # --- dense product -----------------------------------------------------------------------------
 @pytest.mark.parametrize("T,N,K", [
     (1, 1, 32), (1, 17, 96), (2, 16, 128), (5, 100, 160), (12, 33, 1024), (13, 64, 6144),
