@@ -346,8 +346,9 @@ coli_status coli_moe_forward_noalloc(const coli_moe_layer *L, const float *x,
 typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
 
 /* Per-token int8 activations.  x [T][n], row stride ldx -> q [T][n] int8
- * (contiguous, 16-byte aligned) and s [T] fp32: s = max|x| / 127 (fp32
- * division); q = clamp(round_half_even(x / s), -127, 127); s = 0 gives q = 0.
+ * (contiguous, 16-byte aligned) and s [T] fp32: s = max|x| * fl32(1 / 127), one
+ * fp32 product; q = clamp(round_half_even(x / s), -127, 127) with an fp32
+ * division; s = 0 gives q = 0.
  * A row holding a NaN or an infinity gets s = NaN and q = 0, so every product
  * made from it is NaN.  n a positive multiple of 32, at most 131040;
  * 0 <= T <= 2^20. */
@@ -367,9 +368,9 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
 /* y [T][N] = s_t * ws_n * sum_k q[t][k] * w[n][k] (+ bias_n), row stride ldy.
  * q [T][K] and s [T] as coli_quant_act_token gives them, w [N][K] and ws [N]
  * an int8 container (coli_quant_pack with COLI_Q8), bias [N] or NULL.  The
- * sum is exact; it is converted to fp32, multiplied by the product of the
- * scales, the bias is added, and the result is rounded once to y's type (past
- * the largest fp16 value: infinity).  K a positive multiple of 32, at most
+ * sum is exact; it is converted to fp32, multiplied by the channel's scale and
+ * the token's, the bias is added, and the result is rounded once to y's type
+ * (past the largest fp16 value: infinity).  K a positive multiple of 32, at most
  * 131040; 0 <= T <= 2^20; N >= 1; q, w 16-byte aligned.  Sizes whose
  * launch would not fit a grid return COLI_ERR_UNSUPPORTED. */
 coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T,

@@ -142,9 +142,10 @@ __device__ __forceinline__ Tile expert_tile(const Q8Args &a, int nbn) {
   return a.E <= 256 ? expert_tile_n<BM, 4>(a, nbn) : expert_tile_n<BM, 16>(a, nbn);
 }
 
-// y's element from the exact sum.
+// y's element from the exact sum.  (The product of two small scales could be
+// subnormal where the result is not, so the sum comes first.)
 __device__ __forceinline__ float finish(int acc, float st, float sn, float b) {
-  return (float)acc * (st * sn) + b;
+  return (float)acc * sn * st + b;
 }
 
 // s_waitcnt vmcnt(N) lgkmcnt(0) and a barrier.

@@ -2,9 +2,11 @@
 // activations or of SwiGLU's result, and the weighted sum of a token's
 // expert outputs.
 //
-// A row's codes: a = max|x|, s = fl32(a / 127), q = clamp(round_half_even(
-// fl32(x / s)), -127, 127); s = 0 gives q = 0.  This is the rule of the
-// library's other containers with the row as the block.  A row that holds a
+// A row's codes: a = max|x|, s = fl32(a * fl32(1 / 127)), q = clamp(
+// round_half_even(fl32(x / s)), -127, 127); s = 0 gives q = 0.  This is the
+// rule of the library's other containers with the row as the block, but for
+// the scale: one product with the reciprocal, which is how tensor libraries
+// divide by a number, within one unit in the last place of the quotient.  A row that holds a
 // NaN or an infinity has no scale: s = NaN and q = 0, so that every product
 // made from it is NaN and the fault stays visible.
 //
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_quant_token(
     for (int i = 1; i < TR / 64; ++i) amax = max(amax, part[i]);
   }
   const bool bad = amax >= 0x7f800000;
-  const float sc = bad ? __int_as_float(0x7fc00000) : __int_as_float(amax) / 127.f;
+  const float sc = bad ? __int_as_float(0x7fc00000) : __int_as_float(amax) * (1.f / 127.f);
   const float inv = sc > 1e-30f ? 1.f / sc : 0.f;  // 0: divide
   if (tr == 0) s[row] = sc;
   const bool zero = bad || sc == 0.f;

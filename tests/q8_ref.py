@@ -6,12 +6,13 @@ import numpy as np
 
 
 def quant(x: np.ndarray):
-    """Codes and scales of x [T, n] (values of its type, exact in float64)."""
+    """Codes and scales of x [T, n] (values of its type, exact in float64; their
+    largest is a float32)."""
     x = x.astype(np.float64)
     a = np.abs(x).max(axis=1)
     with np.errstate(all="ignore"):
         bad = ~np.isfinite(x).all(axis=1)
-        s = (a / 127.0).astype(np.float32)
+        s = a.astype(np.float32) * (np.float32(1) / np.float32(127))  # one product in binary32
         s64 = s.astype(np.float64)[:, None]
         r = np.where(s64 > 0, x / np.where(s64 > 0, s64, 1.0), 0.0).astype(np.float32)
         q = np.clip(np.rint(r.astype(np.float64)), -127, 127)

@@ -152,14 +152,13 @@ def test_swiglu_far_values():
 
 def test_quant_more_rows_than_one_grid_axis():
     """Over 2^22 rows of 32: workgroups along both axes.  Every row's codes
-    against the definition in torch, each quotient rounded once from float64
-    (torch divides a float32 tensor by a number by multiplying with 1 / number)."""
+    against the definition in torch, each quotient rounded once from float64."""
     T, n = (1 << 22) + 5, 32
     x = torch.randn(T, n, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
     q, s = torch.empty(T, n, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
     B.coli_swiglu_quant_token(torch.full_like(x, 1e4), x, q, s)  # silu(1e4) = 1e4
     h = (x.double() * 1e4).float()
-    rs = (h.abs().amax(1).double() / 127).float()
+    rs = h.abs().amax(1) * float(np.float32(1) / np.float32(127))
     assert torch.equal(s, rs)
     assert torch.equal(q, torch.round((h.double() / rs[:, None].double()).float()).to(torch.int8))
 
@@ -224,6 +223,19 @@ def test_gemm_q8_largest_sums():
     y = torch.empty(70, 70, device="cuda")
     B.coli_gemm_q8(q, torch.ones(70, device="cuda"), w.view(torch.uint8), torch.ones(70, device="cuda"), y)
     assert (f64(y) == float(np.float32(128 * 128 * K))).all()
+
+
+@pytest.mark.parametrize("T,N", [(3, 40), (70, 40), (512, 6144)])
+def test_gemm_q8_small_scales(T, N):
+    """Scales whose product is subnormal where the result is not."""
+    K = 96
+    q, w = codes(T, K, seed=1), codes(N, K, seed=2)
+    s, ws = scales(T) * 1e-34, scales(N, seed=3) * 1e-3
+    y = torch.empty(T, N, device="cuda")
+    B.coli_gemm_q8(q, s, w.view(torch.uint8), ws, y)
+    ref = R.product(q.cpu().numpy(), s.cpu().numpy(), w.cpu().numpy(), ws.cpu().numpy())
+    ok = np.abs(f64(y) - ref) <= 3 * 2.0 ** -24 * np.abs(ref) + 2.0 ** -149  # and one subnormal step
+    assert ok.all()
 
 
 def test_gemm_q8_nan_scale_stays_in_its_row():
