@@ -948,16 +948,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 :
 // workgroups the 256 CUs hold at once.
 // ---------------------------------------------------------------------------
 enum Variant {
-  kRing16x16, kRing16x32, kRing32x32, kRing32x64, kRing64x32, kRing64x32Deep, kRing64x64,
-  kSweep32, kSweep64, kTile128, kTile128Deep, kTile256, kVariants
+  kRing16x16, kRing16x32, kRing32x64, kRing64x32, kRing64x64, kSweep32, kSweep64,
+  kTile128, kTile128Deep, kTile256, kVariants
 };
 struct Shape {
   int bm, bn, threads, slots;
 };
 constexpr Shape kShapes[kVariants] = {
-    {16, 16, 256, 512},   {16, 32, 256, 512},  {32, 32, 256, 512},   {32, 64, 256, 512},
-    {64, 32, 512, 512},   {64, 32, 512, 256},  {64, 64, 512, 512},   {32, 64, 128, 2048},
-    {64, 128, 256, 1024}, {128, 128, 256, 512}, {128, 128, 256, 256}, {256, 256, 512, 256}};
+    {16, 16, 256, 512}, {16, 32, 256, 512},   {32, 64, 256, 512},   {64, 32, 512, 512},   {64, 64, 512, 512},
+    {32, 64, 128, 2048}, {64, 128, 256, 768}, {128, 128, 256, 512}, {128, 128, 256, 256}, {256, 256, 512, 256}};
 
 // Upper bound of the token tiles of bm over E experts with P pairs.
 int64_t max_tiles(const Q8Args &a, int bm) { return a.P / bm + (a.P < a.E ? a.P : a.E); }
@@ -986,31 +985,35 @@ Variant grouped_variant(const Q8Args &a) {
   return kTile256;
 }
 
-// The dense product.  Up to 64 tokens one token tile reads the weights, and
-// the narrower blocks are taken while they leave CUs without a workgroup
-// (6144 columns: 1 token x 2048 channels 5.3 us by 16 x 16 against 5.8 by 16 x
-// 32, 6144 channels 8.1 against 7.5; 61 tokens x 131072 channels 160 us by
-// kSweep64 against 177 by 64 x 64).  More tokens: the least time as measured
-// at 6144 columns, a kernel's time with at most one workgroup a CU or that of
-// a full round of its slots (512 x 6144: kTile128Deep 34 us, 64 x 64 41;
-// 1024: kTile128 50, 64 x 64 68, kTile256 75; 2048: kTile256 85, kTile128 91;
-// 200: 64 x 64 22, kTile128Deep 31).
+// The dense product: the variant of the least time, from what each takes at
+// 4096 columns (in 0.1 us) with at most one workgroup a CU, and for a full
+// round of its slots.  Over 1 to 3000 tokens x 300 to 40000 channels x 1024,
+// 2560 and 6144 columns that is the best variant or within 15 % of it but for
+// one of 150 sizes (3000 x 300 x 6144: 64x32 27 us, 64x64 22).  Some of both
+// sides (us, 6144 columns):
+//   30 x 2048   16x16 7.7, 64x32 10.6              1 x 6144     16x32 9.1, 64x32 11.0
+//   61 x 6144   64x32 12.0, 16x32 17.6             200 x 6144   64x64 22.4, 64x32 26.0
+//   509 x 6144  128x128 of one a CU 33.6,          1500 x 6144  256x256 80.6, 128x128 85.4
+//               of two 37.8, 64x64 40.8            3000 x 6144  128x128 134.6, 256x256 160.6
+// (Blocks whose tokens would be half empty are left out.)  With very many
+// channels all are bound by the memory: 61 x 131072 channels of 6144 columns 160
+// us by the sweep, 177 by 64x64.
 Variant dense_variant(const Q8Args &a) {
-  if (a.rows <= 16) return a.N <= 4096 ? kRing16x16 : kRing16x32;
-  if (a.rows <= 32) return a.N <= 8192 ? kRing32x32 : kRing32x64;
-  if (a.rows <= 64)
-    return a.N <= 8192 ? kRing64x32Deep : a.N >= 65536 ? kSweep64 : kRing64x32;
   struct Time {
     Variant v;
     int first, round;
   };
-  constexpr Time kTimes[] = {{kRing64x32, 11, 17}, {kRing64x64, 19, 25}, {kTile128Deep, 31, 1000},
-                             {kTile128, 35, 50},   {kTile256, 72, 86}};
+  constexpr Time kTimes[] = {{kRing16x16, 58, 70},   {kRing16x32, 67, 82},       {kRing32x64, 108, 140},
+                             {kRing64x32, 83, 138},  {kRing64x64, 140, 185},     {kTile128Deep, 240, 0},
+                             {kTile128, 265, 410},   {kTile256, 565, 693}};
+  if (a.rows > 32 && a.rows <= 64 && a.N >= 65536) return kSweep64;
   Variant best = kTile256;
   int64_t least = INT64_MAX;
   for (const Time &t : kTimes) {
-    const int64_t n = workgroups(a, t.v), slots = kShapes[t.v].slots;
-    const int64_t cost = n <= 256 ? t.first : t.round * ((n + slots - 1) / slots);
+    const Shape &s = kShapes[t.v];
+    const int64_t n = workgroups(a, t.v);
+    if ((s.bm > 16 && s.bm >= 2 * (int64_t)a.rows) || (n > 256 && t.round == 0)) continue;
+    const int64_t cost = n <= 256 ? t.first : t.round * ((n + s.slots - 1) / s.slots);
     if (cost < least) {
       least = cost;
       best = t.v;
@@ -1068,10 +1071,8 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
       switch (v) {
         case kRing16x16: run_ring<DT, false, 16, 16, 1, 1, 4, 8>(a, wgs, st); break;
         case kRing16x32: run_ring<DT, false, 16, 32, 1, 1, 4, 6>(a, wgs, st); break;
-        case kRing32x32: run_ring<DT, false, 32, 32, 1, 1, 4, 4>(a, wgs, st); break;
         case kRing32x64: run_ring<DT, false, 32, 64, 1, 1, 4, 3>(a, wgs, st); break;
         case kRing64x32: run_ring<DT, false, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
-        case kRing64x32Deep: run_ring<DT, false, 64, 32, 2, 1, 4, 6>(a, wgs, st); break;
         case kRing64x64: run_ring<DT, false, 64, 64, 2, 2, 2, 2>(a, wgs, st); break;
         case kSweep64: run_sweep<DT, false, 64, 4, 3>(a, wgs, st); break;
         case kTile128: run_tile<DT, false, 128, 128, 2, 2, 128, 64 << 10>(a, wgs, st); break;
