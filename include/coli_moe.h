@@ -394,10 +394,15 @@ coli_status coli_gemm_q8_grouped(const int8_t *q, const float *s, int32_t rows,
                                  int32_t dtype, void *y, int64_t ldy,
                                  void *stream);
 
+/* Added to coli_moe_combine's dtype: o is fp32, whatever the type of add and
+ * y, so that the experts' products are not rounded before they are summed. */
+#define COLI_COMBINE_O_F32 16
+
 /* y [T][H] = add[t] + sum_j w[t][j] * o[t * k + j], in slot order and fp32,
  * rounded once.  o [T * k][H], w [T][k]; idx [T][k] or NULL: slots with a
  * negative idx are not read.  add [T][H] (for example the shared expert's
- * output) or NULL; it may be y itself.  1 <= k <= 32, 1 <= H <= 131072,
+ * output) or NULL; it may be y itself.  o, add and y are of type dtype, or o
+ * is fp32 with dtype | COLI_COMBINE_O_F32.  1 <= k <= 32, 1 <= H <= 131072,
  * 0 <= T <= 2^20. */
 coli_status coli_moe_combine(int32_t dtype, const void *o, int64_t ldo,
                              const int32_t *idx, const float *w, int32_t T,

@@ -21,6 +21,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "coli_moe.h")
 COLI_OK, COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, COLI_ERR_WORKSPACE, COLI_ERR_DEVICE = range(5)
 COLI_Q8, COLI_Q4, COLI_Q2 = 8, 4, 2
 COLI_F32, COLI_BF16, COLI_F16 = range(3)
+COLI_COMBINE_O_F32 = 16
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 GROUP_TOP2, GROUP_MAX = 0, 1
 
@@ -436,12 +437,17 @@ def coli_moe_combine(o: torch.Tensor, idx: torch.Tensor | None, w: torch.Tensor,
                      add: torch.Tensor | None = None, stream=None) -> None:
     """y [T, H] = add + sum_j w[:, j] * o[t * k + j] over the slots whose idx is
     not negative; o [T * k, H], idx int32 [T, k] or None, w fp32 [T, k], add
-    [T, H] or None (all of one float type; rows may be strided)."""
+    [T, H] or None (of y's float type, o of that or float32; rows may be strided).
+    In float32, o keeps the experts' products as they were computed; in a
+    16-bit type each of them is rounded before the sum."""
     dev = _device_of(o, "o")
     T, k = w.shape
     H = y.shape[1]
     dt = _float_type(y, "y")
-    op, ldo = _rowed(o, T * k, H, y.dtype, dev, "o")
+    odt = torch.float32 if o.dtype is torch.float32 else y.dtype
+    op, ldo = _rowed(o, T * k, H, odt, dev, "o")
+    if odt is not y.dtype:
+        dt |= COLI_COMBINE_O_F32
     yp, ldy = _rowed(y, T, H, y.dtype, dev, "y")
     ap, lda = (None, 0) if add is None else _rowed(add, T, H, y.dtype, dev, "add")
     _check("coli_moe_combine", lib().coli_moe_combine(

@@ -481,15 +481,17 @@ coli_status coli_moe_combine(int32_t dtype, const void *o, int64_t ldo, const in
                              const float *w, int32_t T, int32_t k, int32_t H, const void *add,
                              int64_t ldadd, void *y, int64_t ldy, void *stream) {
   return guarded([&] {
+    const int32_t o_dtype = dtype >= 0 && dtype & COLI_COMBINE_O_F32 ? (int32_t)COLI_F32 : dtype;
+    if (dtype >= 0) dtype &= ~COLI_COMBINE_O_F32;
     if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || k < 1 || k > 32 || H < 1 || H > 131072)
       return COLI_ERR_INVALID_ARG;
     if (T == 0) return COLI_OK;
-    if (!rows_ok(dtype, o, ldo, H) || !rows_ok(dtype, y, ldy, H) || !w || !aligned(w, 4) ||
+    if (!rows_ok(o_dtype, o, ldo, H) || !rows_ok(dtype, y, ldy, H) || !w || !aligned(w, 4) ||
         !aligned(idx, 4) || (add && !rows_ok(dtype, add, ldadd, H)))
       return COLI_ERR_INVALID_ARG;
     const coli_status st = check_device();
     if (st != COLI_OK) return st;
-    return from_hip(coli::launch_combine_rows(dtype, o, ldo, idx, w, T, k, H, add, ldadd, y, ldy,
+    return from_hip(coli::launch_combine_rows(dtype, o_dtype, o, ldo, idx, w, T, k, H, add, ldadd, y, ldy,
                                               static_cast<hipStream_t>(stream)));
   });
 }

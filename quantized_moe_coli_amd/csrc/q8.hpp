@@ -42,8 +42,9 @@ inline hipError_t by_dtype(int dt, F &&fn) {
 hipError_t launch_quant_token(int dt, const void *x, int64_t ldx, const void *u, int64_t ldu, int T,
                               int n, int8_t *q, float *s, hipStream_t st);
 
-// y[t] = (add ? add[t] : 0) + sum_j w[t][j] * o[t * k + j].
-hipError_t launch_combine_rows(int dt, const void *o, int64_t ldo, const int32_t *idx, const float *w,
+// y[t] = (add ? add[t] : 0) + sum_j w[t][j] * o[t * k + j]; o of type odt, which
+// is dt or COLI_F32.
+hipError_t launch_combine_rows(int dt, int odt, const void *o, int64_t ldo, const int32_t *idx, const float *w,
                                int T, int k, int H, const void *add, int64_t ldadd, void *y,
                                int64_t ldy, hipStream_t st);
 

@@ -153,13 +153,15 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_quant_token(
 
 // y[t][h] = (add[t][h]) + sum_j w[t][j] o[t k + j][h], slots in order, in
 // binary32, rounded once to the type.  A slot whose idx is -1 is not read:
-// its row of o may hold anything.
-template <int DT, int N>
+// its row of o may hold anything.  o is of y's type or binary32.
+template <int DT, int ODT, int N>
 __global__ __launch_bounds__(256) void k_combine_rows(
-    const typename Elem<DT>::type *__restrict__ o, int64_t ldo, const int32_t *__restrict__ idx,
+    const typename Elem<ODT>::type *__restrict__ o, int64_t ldo, const int32_t *__restrict__ idx,
     const float *__restrict__ w, int k, int H, const typename Elem<DT>::type *add, int64_t ldadd,
     typename Elem<DT>::type *y, int64_t ldy) {
   typedef typename Elem<DT>::type T;
+  typedef typename Elem<ODT>::type O;
+  constexpr int NO = N * (int)sizeof(O) > 16 ? 16 / (int)sizeof(O) : N;  // elements of a load of o
   const int t = blockIdx.x;
   const int h = (blockIdx.y * 256 + threadIdx.x) * N;
   if (h >= H) return;
@@ -175,9 +177,12 @@ __global__ __launch_bounds__(256) void k_combine_rows(
     const int64_t p = (int64_t)t * k + j;
     if (idx && idx[p] < 0) continue;
     const float wj = w[p];
-    const Pack<T, N> a = *reinterpret_cast<const Pack<T, N> *>(o + p * ldo + h);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = fmaf(wj, (float)a.v[i], acc[i]);
+    for (int g = 0; g < N / NO; ++g) {
+      const Pack<O, NO> a = reinterpret_cast<const Pack<O, NO> *>(o + p * ldo + h)[g];
+#pragma unroll
+      for (int i = 0; i < NO; ++i) acc[g * NO + i] = fmaf(wj, (float)a.v[i], acc[g * NO + i]);
+    }
   }
   Pack<T, N> r;
 #pragma unroll
@@ -227,7 +232,7 @@ hipError_t launch_quant_token(int dt, const void *x, int64_t ldx, const void *u,
   });
 }
 
-hipError_t launch_combine_rows(int dt, const void *o, int64_t ldo, const int32_t *idx, const float *w,
+hipError_t launch_combine_rows(int dt, int odt, const void *o, int64_t ldo, const int32_t *idx, const float *w,
                                int T, int k, int H, const void *add, int64_t ldadd, void *y,
                                int64_t ldy, hipStream_t st) {
   if (T == 0) return hipSuccess;
@@ -235,18 +240,22 @@ hipError_t launch_combine_rows(int dt, const void *o, int64_t ldo, const int32_t
     constexpr int DT = decltype(dtc)::value;
     typedef typename Elem<DT>::type E;
     constexpr int N = 16 / (int)sizeof(E);
-    auto go = [&](auto nc) {
-      constexpr int NN = decltype(nc)::value;
+    auto go = [&](auto odtc, auto nc) {
+      constexpr int ODT = decltype(odtc)::value, NN = decltype(nc)::value;
       const int per_row = (H + 256 * NN - 1) / (256 * NN);
-      hipLaunchKernelGGL((k_combine_rows<DT, NN>), dim3(T, per_row), dim3(256), 0, st,
-                         static_cast<const E *>(o), ldo, idx, w, k, H, static_cast<const E *>(add),
-                         ldadd, static_cast<E *>(y), ldy);
+      hipLaunchKernelGGL((k_combine_rows<DT, ODT, NN>), dim3(T, per_row), dim3(256), 0, st,
+                         static_cast<const typename Elem<ODT>::type *>(o), ldo, idx, w, k, H,
+                         static_cast<const E *>(add), ldadd, static_cast<E *>(y), ldy);
     };
-    if (H % N == 0 && rows_aligned<DT>(o, ldo, 16) && rows_aligned<DT>(y, ldy, 16) &&
-        (!add || rows_aligned<DT>(add, ldadd, 16)))
-      go(std::integral_constant<int, N>());
-    else
-      go(std::integral_constant<int, 1>());
+    auto by_width = [&](auto odtc) {
+      if (H % N == 0 && rows_aligned<decltype(odtc)::value>(o, ldo, 16) && rows_aligned<DT>(y, ldy, 16) &&
+          (!add || rows_aligned<DT>(add, ldadd, 16)))
+        go(odtc, std::integral_constant<int, N>());
+      else
+        go(odtc, std::integral_constant<int, 1>());
+    };
+    if (odt == dt) by_width(dtc);
+    else by_width(std::integral_constant<int, COLI_F32>());
     return hipGetLastError();
   });
 }

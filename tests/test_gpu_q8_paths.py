@@ -1,0 +1,74 @@
+"""The 8-bit operators on the paths that a model's layers take: results of the
+types and strides that are stored in 16-byte words, rings that come round
+several times, tokens in batches of any size.  Against 64-bit forms, with the
+tolerances that test_gpu_q8.py derives.
+"""
+import numpy as np
+import pytest
+import torch
+
+import q8_ref as R
+from quantized_moe_coli_amd import binding as B
+from test_gpu_q8 import DT, acts, assert_product, codes, f64, gen, half_step, routing, scales
+
+pytestmark = pytest.mark.gpu
+
+
+# --- combine of float32 rows -------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,H,pad,add", [(1, 1, 1, 0, False), (3, 8, 6144, 0, False), (5, 2, 100, 4, True),
+                                           (2, 32, 515, 0, True), (700, 3, 64, 0, True), (4, 2, 2064, 4, True),
+                                           (2, 4, 33, 1, False), (3, 2, 512, 2, False)])
+def test_combine_of_float32_rows(dt, T, k, H, pad, add):
+    """At most k roundings of partial sums in binary32, each no larger than the
+    sum of the terms' sizes, and the result's rounding to its type: the rows
+    themselves are not rounded."""
+    o = acts(T * k, H, torch.float32, 4, pad)
+    w = torch.randn(T, k, generator=gen(T, k)).cuda()
+    idx = torch.randint(-1, 3, (T, k), generator=gen(T, k, 2), dtype=torch.int32)
+    on = (idx >= 0).numpy()
+    o[torch.from_numpy(~on.ravel()).cuda()] = float("nan")  # rows that are not read
+    a = acts(T, H, DT[dt], 6) if add else None
+    y = torch.empty(T, H, dtype=DT[dt], device="cuda")
+    B.coli_moe_combine(o, idx.cuda(), w, y, add=a)
+    terms = np.where(on[:, :, None], f64(o).reshape(T, k, H) * f64(w)[:, :, None], 0.0)
+    ref = terms.sum(1) + (f64(a) if add else 0.0)
+    size = np.abs(terms).sum(1) + (np.abs(f64(a)) if add else 0.0)
+    tol = k * 2.0 ** -24 * size * 1.01
+    tol = tol + half_step(DT[dt]) * (np.abs(ref) + tol) + (2.0 ** -25 if dt == "f16" else 0.0)
+    assert (np.abs(f64(y) - ref) <= tol).all()
+    if add:  # in place
+        B.coli_moe_combine(o, idx.cuda(), w, a, add=a)
+        assert torch.equal(a, y)
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 8, 16, 264, 96), (45, 4, 8, 512, 160), (300, 2, 3, 260, 64)])
+def test_experts_product_in_float32_and_its_sum_in_bf16(T, k, E, N, K):
+    """The experts' second product with float32 results and their sum in bf16:
+    one rounding to bf16 from the 64-bit definition, beside what binary32 adds
+    (a product's three roundings and the k of the sum, relative to the terms)."""
+    idx = routing(T, k, E, 5, 0.2)
+    offs, perm = (torch.from_numpy(v).cuda() for v in R.tables(idx.numpy(), E))
+    P = T * k
+    q, s, w, ws = codes(P, K, seed=1), scales(P), codes(E, N, K, seed=2), scales(E, N)
+    wt = torch.rand(T, k, generator=gen(T, k)).cuda()
+    o, y = torch.full((P, N), float("nan"), device="cuda"), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    B.coli_gemm_q8_grouped(q, s, w.view(torch.uint8), ws, offs, perm, o)
+    B.coli_moe_combine(o, idx.cuda(), wt, y)
+    flat, terms = idx.numpy().ravel(), np.zeros((P, N))
+    for e in range(E):
+        r = np.flatnonzero(flat == e)
+        terms[r] = R.product(q.cpu().numpy()[r], s.cpu().numpy()[r], w[e].cpu().numpy(), ws[e].cpu().numpy())
+    terms = terms.reshape(T, k, N) * f64(wt)[:, :, None]
+    ref, size = terms.sum(1), np.abs(terms).sum(1)
+    tol = (k + 3) * 2.0 ** -24 * 1.01 * size
+    tol = tol + half_step(torch.bfloat16) * (np.abs(ref) + tol)
+    assert (np.abs(f64(y) - ref) <= tol).all()
+
+
+def test_combine_refuses_rows_of_another_16_bit_type():
+    w, y = torch.rand(2, 2).cuda(), torch.empty(2, 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="o must be torch.bfloat16"):
+        B.coli_moe_combine(acts(4, 8, torch.float16), None, w, y)
+    with pytest.raises(ValueError, match="add must be torch.bfloat16"):
+        B.coli_moe_combine(acts(4, 8, torch.float32), None, w, y, add=acts(2, 8, torch.float32))
