@@ -159,6 +159,8 @@ def prepare(case, seed):
     if own:
         import quantized_moe_coli_amd as C
         s["C"] = C
+        if case["op"] == "experts_out":  # the products as they are computed: only their sum is rounded
+            s["o32"] = torch.empty(T * case["top_k"], N, device="cuda")
     if case["op"] == "linear":
         s["x"] = _acts(T, K, dt, g, case["pad"])
         s["w"], s["ws"] = _codes((N, K), g), _scales(N, g)
@@ -217,8 +219,8 @@ def _run_own(s):
                                fan=s["case"]["top_k"])
         return s["y"]
     C.coli_swiglu_quant_token(s["g"], s["u"], s["q"], s["qs"])
-    C.coli_gemm_q8_grouped(s["q"], s["qs"], s["w"], s["ws"], s["offs"], s["perm"], s["o"])
-    C.coli_moe_combine(s["o"], s["idx"], s["wt"], s["y"])
+    C.coli_gemm_q8_grouped(s["q"], s["qs"], s["w"], s["ws"], s["offs"], s["perm"], s["o32"])
+    C.coli_moe_combine(s["o32"], s["idx"], s["wt"], s["y"])
     return s["y"]
 
 
