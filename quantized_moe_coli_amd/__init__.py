@@ -17,7 +17,5 @@ def __getattr__(name):
         return importlib.import_module("." + name, __name__)
     if name.startswith("__"):
         raise AttributeError(name)
-    value = getattr(importlib.import_module(".binding", __name__), name)
-    if callable(value):  # functions and classes: later accesses are plain lookups
-        globals()[name] = value
-    return value
+    # (the import system has set ``binding`` here once it was loaded)
+    return getattr(globals().get("binding") or importlib.import_module(".binding", __name__), name)
