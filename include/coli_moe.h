@@ -368,9 +368,10 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
 /* y [T][N] = s_t * ws_n * sum_k q[t][k] * w[n][k] (+ bias_n), row stride ldy.
  * q [T][K] and s [T] as coli_quant_act_token gives them, w [N][K] and ws [N]
  * an int8 container (coli_quant_pack with COLI_Q8), bias [N] or NULL.  The
- * sum is exact; it is converted to fp32, multiplied by the channel's scale and
- * the token's, the bias is added, and the result is rounded once to y's type
- * (past the largest fp16 value: infinity).  K a positive multiple of 32, at most
+ * sum is exact; it is converted to fp32 and multiplied by the channel's scale;
+ * the product by the token's scale and the bias's addition are one fused
+ * step, rounded to fp32 (and that to bf16) or to fp16 (past its largest value:
+ * infinity).  A token's row does not depend on the batch it is in.  K a positive multiple of 32, at most
  * 131040; 0 <= T <= 2^20; N >= 1; q, w 16-byte aligned.  Sizes whose
  * launch would not fit a grid return COLI_ERR_UNSUPPORTED. */
 coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T,

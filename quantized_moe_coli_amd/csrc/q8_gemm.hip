@@ -5,8 +5,9 @@
 // Unlike a product against Q8_0 blocks, no scale changes along k, so the
 // whole sum stays in the int32 accumulators of the matrix instructions and
 // is exact for K < 2^17 (128 * 128 * K < 2^31); one conversion and two
-// multiplications in binary32 finish it, and one rounding to y's type.
-// Exact sums also make every split of k give the same bits.
+// multiplications in binary32 (the second fused with the bias's addition)
+// finish it, and a rounding to y's type.  Exact sums also make every split
+// of k, and so every kernel below, give the same bits.
 //
 // Both operands are contiguous along k, which is what the instructions take:
 // v_mfma_i32_32x32x32_i8 reads 16 consecutive bytes of row (lane % 32) at
@@ -24,6 +25,8 @@
 #include <type_traits>
 
 #include "q8.hpp"
+
+#pragma clang fp contract(off)
 
 namespace coli {
 namespace {
@@ -143,9 +146,12 @@ __device__ __forceinline__ Tile expert_tile(const Q8Args &a, int nbn) {
 }
 
 // y's element from the exact sum.  (The product of two small scales could be
-// subnormal where the result is not, so the sum comes first.)
+// subnormal where the result is not, so the sum comes first.  The last
+// product and the bias's addition are one rounding by the source's own word,
+// not by the compiler's choice in each kernel.  To fp16 they are one
+// instruction, which rounds the exact value straight to fp16.)
 __device__ __forceinline__ float finish(int acc, float st, float sn, float b) {
-  return (float)acc * sn * st + b;
+  return __builtin_fmaf((float)acc * sn, st, b);
 }
 
 // s_waitcnt vmcnt(N) lgkmcnt(0) and a barrier.

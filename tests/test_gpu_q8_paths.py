@@ -72,3 +72,66 @@ def test_combine_refuses_rows_of_another_16_bit_type():
         B.coli_moe_combine(acts(4, 8, torch.float16), None, w, y)
     with pytest.raises(ValueError, match="add must be torch.bfloat16"):
         B.coli_moe_combine(acts(4, 8, torch.float32), None, w, y, add=acts(2, 8, torch.float32))
+
+
+# --- one definition in every kernel ------------------------------------------------------------
+def fused(x, s, b):
+    """x * s + b of float32 arrays in binary64, the product exact and the sum
+    rounded to odd (where it is inexact, to the neighbour with an odd last
+    place), so that a rounding to fewer bits is that of the exact value."""
+    p, b = x.astype(np.float64) * s.astype(np.float64), b.astype(np.float64)
+    v = p + b
+    t = v - p
+    err = (p - (v - t)) + (b - t)
+    even = (v.view(np.int64) & 1) == 0
+    v = np.where((err != 0) & even, np.nextafter(v, np.where(err > 0, np.inf, -np.inf)), v)
+    return v
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("bias", [False, True])
+def test_a_tokens_result_is_the_same_in_every_batch(dt, bias):
+    """Batches and numbers of channels that take each kernel of the dense
+    product: a token's channels have the same bits in all of them, and those of
+    the definition: sum, conversion, channel's scale, and the token's scale and
+    the bias in one step to float32 and from there to bf16, or to fp16."""
+    K, N = 416, 65536
+    q, s = codes(1500, K, seed=1), scales(1500)
+    w, ws = codes(N, K, seed=2), scales(N, seed=3)
+    b = torch.randn(N, generator=gen(N)).cuda() if bias else None
+    y = {}
+    for T, n in ((1, 2064), (1, 6144), (45, 6144), (130, 6144), (200, 6144), (512, 6144), (1021, 6144),
+                 (1500, 6144), (45, N)):
+        r = torch.empty(T, n, dtype=DT[dt], device="cuda")
+        B.coli_gemm_q8(q[:T], s[:T], w[:n].view(torch.uint8), ws[:n], r, bias=b[:n] if bias else None)
+        y[T, n] = r
+    most = y[1500, 6144]
+    for (T, n), r in y.items():
+        m = min(n, 6144)
+        assert torch.equal(r[:, :m], most[:T, :m]), (T, n)
+    t, n = 160, 400
+    acc = (f64(q[:t]) @ f64(w[:n]).T).astype(np.float32)
+    sn, st = ws[:n].cpu().numpy()[None], s[:t].cpu().numpy()[:, None]
+    bn = b[:n].cpu().numpy()[None] if bias else np.zeros((1, 1), np.float32)
+    ref = fused((acc * sn).astype(np.float32), st, bn)
+    ref = torch.from_numpy(ref.astype(np.float16 if dt == "f16" else np.float32)).to(DT[dt])
+    assert torch.equal(most[:t, :n].cpu(), ref)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_a_pairs_result_is_the_same_in_every_batch(dt):
+    """The same over experts: each kernel gives a pair the bits that the dense
+    product gives its token."""
+    K, N = 416, 2048
+    w, ws = codes(40, N, K, seed=2), scales(40, N, seed=3)
+    q, s = codes(2400, K, seed=1), scales(2400)
+    for E, per in ((40, 2), (2, 3), (40, 40), (2, 40), (4, 60), (3, 700)):
+        P = E * per
+        offs = (torch.arange(E + 1) * per).to(torch.int32).cuda()
+        y = torch.empty(P, N, dtype=DT[dt], device="cuda")
+        B.coli_gemm_q8_grouped(q[:P], s[:P], w[:E].view(torch.uint8), ws[:E], offs,
+                               torch.arange(P, dtype=torch.int32).cuda(), y)
+        for e in range(E):
+            r = torch.empty(per, N, dtype=DT[dt], device="cuda")
+            B.coli_gemm_q8(q[e * per:(e + 1) * per], s[e * per:(e + 1) * per], w[e].view(torch.uint8), ws[e], r)
+            assert torch.equal(y[e * per:(e + 1) * per], r), (E, per, e)
