@@ -348,7 +348,9 @@ typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
 /* Per-token int8 activations.  x [T][n], row stride ldx -> q [T][n] int8
  * (contiguous, 16-byte aligned) and s [T] fp32: s = max|x| * fl32(1 / 127), one
  * fp32 product; q = clamp(round_half_even(x / s), -127, 127) with an fp32
- * division; s = 0 gives q = 0.
+ * division; s = 0 gives q = 0.  (127 * fl32(1 / 127) is 1 - 2^-28, so s is
+ * within 1.07 half-steps of max|x| / 127 and within one unit in the last
+ * place of coli_quant_act_q8_0's quotient; codes are no further from x.)
  * A row holding a NaN or an infinity gets s = NaN and q = 0, so every product
  * made from it is NaN.  n a positive multiple of 32, at most 131040;
  * 0 <= T <= 2^20. */

@@ -135,3 +135,23 @@ def test_a_pairs_result_is_the_same_in_every_batch(dt):
             r = torch.empty(per, N, dtype=DT[dt], device="cuda")
             B.coli_gemm_q8(q[e * per:(e + 1) * per], s[e * per:(e + 1) * per], w[e].view(torch.uint8), ws[e], r)
             assert torch.equal(y[e * per:(e + 1) * per], r), (E, per, e)
+
+
+# --- the token's scale -------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", DT)
+def test_token_scale_against_the_quotient(dt):
+    """s = fl(a c) with c = fl(1 / 127) and 127 c = 1 - 2^-28: off a / 127 by at
+    most 2^-24 + 2^-28 of it.  With both roundings of a code's quotient, the
+    value q s is off x by at most half a scale and 127 * 2^-24 of it (the
+    quotient's rounding; at the row's largest, a / s <= 127 (1 + 2^-23))."""
+    c = float(np.float32(1) / np.float32(127))
+    assert 127 * c == 1 - 2.0 ** -28
+    T, n = 2000, 256
+    x = acts(T, n, DT[dt], 12)
+    q, s = torch.empty(T, n, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    B.coli_quant_act_token(x, q, s)
+    x, s = f64(x), f64(s)
+    a = np.abs(x).max(1)
+    assert (np.abs(s - a / 127) <= (2.0 ** -24 + 2.0 ** -28) * (1 + 2.0 ** -24) * a / 127).all()
+    off = np.abs(x - f64(q) * s[:, None])
+    assert (off <= s[:, None] * (0.5 + 127 * 2.0 ** -23)).all()
