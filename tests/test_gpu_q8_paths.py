@@ -155,3 +155,65 @@ def test_token_scale_against_the_quotient(dt):
     assert (np.abs(s - a / 127) <= (2.0 ** -24 + 2.0 ** -28) * (1 + 2.0 ** -24) * a / 127).all()
     off = np.abs(x - f64(q) * s[:, None])
     assert (off <= s[:, None] * (0.5 + 127 * 2.0 ** -23)).all()
+
+
+# --- results stored in 16-byte words -----------------------------------------------------------
+def padded(rows, cols, pad, dt):
+    """[rows, cols] of a wider buffer whose other columns hold 77, and these."""
+    wide = torch.full((rows, cols + pad), 77.0, dtype=dt, device="cuda")
+    return wide[:, :cols], wide[:, cols:]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,N,K,pad", [
+    # rows of whole words, and rows that end inside one (their stride is of whole
+    # words): 16 x 16, 16 x 32, 32 x 64, 64 x 32, 64 x 64, the tiles, the sweep
+    (1, 2048, 416, 0), (13, 2049, 96, 7), (3, 6144, 160, 8), (3, 6145, 160, 7), (130, 6152, 160, 0),
+    (130, 6147, 96, 5), (61, 6144, 544, 0), (61, 6145, 352, 7), (200, 6144, 96, 0), (200, 6145, 160, 7),
+    (509, 6144, 288, 0), (512, 6145, 160, 7), (700, 6144, 416, 0), (1021, 6145, 96, 7), (1500, 6145, 160, 7),
+    (2047, 6144, 96, 0), (64, 65536, 160, 0), (45, 65545, 96, 7)])
+def test_dense_results_in_whole_words(dt, T, N, K, pad):
+    q, w, s, ws = codes(T, K, seed=1), codes(N, K, seed=2), scales(T), scales(N, seed=3)
+    y, rest = padded(T, N, pad, DT[dt])
+    B.coli_gemm_q8(q, s, w.view(torch.uint8), ws, y)
+    assert_product(y, R.product(q.cpu().numpy(), s.cpu().numpy(), w.cpu().numpy(), ws.cpu().numpy()), DT[dt])
+    assert (rest == 77.0).all()
+
+
+def check_experts(counts, N, K, dt, pad, fan=1, seed=1):
+    """The experts' product with counts[e] pairs of expert e in any order, and
+    five of no expert, into rows of a wider buffer."""
+    E, P = len(counts), sum(counts) + 5
+    e_of = np.concatenate([np.repeat(np.arange(E), counts), np.full(5, -1)])
+    e_of = e_of[torch.randperm(P, generator=gen(P, seed)).numpy()]
+    offs, perm = (torch.from_numpy(v).cuda() for v in R.tables(e_of[:, None], E))
+    rows = (P + fan - 1) // fan
+    q, s, w, ws = codes(rows, K, seed=1), scales(rows), codes(E, N, K, seed=2), scales(E, N)
+    y, rest = padded(P, N, pad, DT[dt])
+    B.coli_gemm_q8_grouped(q, s, w.view(torch.uint8), ws, offs, perm, y, fan=fan)
+    qn, sn = q.cpu().numpy(), s.cpu().numpy()
+    for e in range(E):
+        p = np.flatnonzero(e_of == e)
+        if len(p):
+            ref = R.product(qn[p // fan], sn[p // fan], w[e].cpu().numpy(), ws[e].cpu().numpy())
+            assert_product(y[torch.from_numpy(p).cuda()], ref, DT[dt])
+    assert (y[torch.from_numpy(np.flatnonzero(e_of < 0)).cuda()] == 77.0).all() and (rest == 77.0).all()
+
+
+def spread(E, per):
+    """E counts around ``per``, one of them zero and one of them one."""
+    c = [max(2, per * (3 + e % 7) // 6) for e in range(E)]
+    c[E // 2], c[E // 3] = 0, 1
+    return c
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E,per,N,K,pad", [
+    # 16 x 32, 64 x 32, the sweeps of 32 and 64 tokens, the tile: rows of whole
+    # words, rows that end inside one, rows of no alignment
+    (9, 4, 264, 96, 0), (9, 4, 257, 160, 7), (9, 4, 260, 96, 1), (9, 40, 264, 160, 0), (9, 40, 257, 96, 7),
+    (9, 40, 260, 96, 1), (65, 5, 1104, 96, 0), (65, 5, 1097, 160, 7), (65, 5, 1104, 96, 3),
+    (66, 25, 1104, 160, 0), (66, 25, 1097, 96, 7), (66, 25, 1104, 96, 3), (4, 150, 264, 96, 0),
+    (4, 150, 257, 160, 7), (4, 150, 260, 96, 1)])
+def test_experts_results_in_whole_words(dt, E, per, N, K, pad):
+    check_experts(spread(E, per), N, K, dt, pad, fan=1 + per % 2)
