@@ -217,3 +217,36 @@ def spread(E, per):
     (4, 150, 257, 160, 7), (4, 150, 260, 96, 1)])
 def test_experts_results_in_whole_words(dt, E, per, N, K, pad):
     check_experts(spread(E, per), N, K, dt, pad, fan=1 + per % 2)
+
+
+# --- rings that come round several times --------------------------------------------------------
+@pytest.mark.parametrize("T,N,K", [
+    # many stages of each dense kernel, with a part stage at the end and without:
+    # 16 x 16 (8 stages of 256), 16 x 32 (6), 32 x 64 and 64 x 32 (3), 64 x 64
+    # (2), the tiles (2 or 3 of 128, 4 with one workgroup a CU), the sweep (4 chunks)
+    (3, 70, 6176), (13, 4096, 6144), (16, 6145, 4128), (130, 6147, 2080), (61, 8200, 2080), (64, 6144, 2048),
+    (200, 6145, 1568), (512, 6145, 2080), (509, 6144, 2048), (700, 6145, 2080), (1500, 6145, 2080),
+    (1505, 6144, 1024), (45, 65536, 2080), (33, 65537, 2048)])
+def test_dense_rings_come_round(T, N, K):
+    q, w, s, ws = codes(T, K, seed=1), codes(N, K, seed=2), scales(T), scales(N, seed=3)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    B.coli_gemm_q8(q, s, w.view(torch.uint8), ws, y)
+    at = torch.randperm(N, generator=gen(N))[:2500]  # every channel block is compared in some row
+    ref = R.product(q.cpu().numpy(), s.cpu().numpy(), w.cpu()[at].numpy(), ws.cpu()[at].numpy())
+    assert_product(y[:, at.cuda()], ref, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fan", [1, 2])
+@pytest.mark.parametrize("counts,N,K", [
+    # the tile with 1 to 8 groups of 32 tokens for a wave, and two tiles of an
+    # expert: 2 to 4 stages of 128 bytes
+    ([20, 40, 70, 100, 140, 170, 200, 256, 290], 260, 2080), ([31, 64, 90, 127, 150, 191, 220, 230, 513], 300, 2048),
+    ([20, 40, 70, 100, 140, 170, 200, 256, 290], 60, 1056),
+    # the rings of 16 and 64 tokens (3 stages of 256 bytes)
+    ([1, 0, 16, 5, 17, 3], 70, 2080), ([2, 9, 0, 30], 45, 6144), ([33, 64, 20, 70, 1], 70, 2080),
+    ([50, 12, 65], 40, 4096),
+    # the sweeps of 32 and 64 tokens (chunks of 128 bytes, 4 and 3 ahead)
+    (spread(65, 5), 1100, 2432), (spread(64, 11), 1024, 2400), (spread(66, 25), 1030, 2432),
+    (spread(64, 45), 1024, 2048)])
+def test_experts_rings_come_round(counts, N, K, fan):
+    check_experts(counts, N, K, "bf16", 0, fan=fan)
