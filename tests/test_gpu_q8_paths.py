@@ -9,7 +9,8 @@ import torch
 
 import q8_ref as R
 from quantized_moe_coli_amd import binding as B
-from test_gpu_q8 import DT, acts, assert_product, codes, f64, gen, half_step, routing, scales
+from test_gpu_q8 import (DT, acts, assert_product, check_route, codes, f64, gen, half_step, routing,
+                         scales)
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +251,21 @@ def test_dense_rings_come_round(T, N, K):
     (spread(64, 45), 1024, 2048)])
 def test_experts_rings_come_round(counts, N, K, fan):
     check_experts(counts, N, K, "bf16", 0, fan=fan)
+
+
+# --- routing of large fp16 batches ---------------------------------------------------------------
+@pytest.mark.parametrize("score,gs", [("softmax", "max"), ("softmax", "top2"), ("sigmoid", "top2"),
+                                      ("sigmoid", "max")])
+@pytest.mark.parametrize("T,E,k,G,TG", [(1024, 256, 8, 1, 1), (1029, 256, 8, 8, 4), (2050, 60, 6, 4, 2),
+                                        (1025, 16, 9, 16, 9), (4097, 45, 5, 9, 3), (1027, 257, 16, 1, 1)])
+def test_route_scored_fp16_batches(score, gs, T, E, k, G, TG):
+    """fp16 logits (many of them equal), dead experts, rows without any, rows of
+    the type's lowest value, rows of a wider buffer."""
+    g = gen(T, E, k)
+    wide = (torch.randn(T, E + 3, generator=g) * 2).to(torch.float16)
+    wide[::3] = torch.randint(-3, 4, (len(range(0, T, 3)), E + 3), generator=g).to(torch.float16)
+    wide[torch.rand(T, E + 3, generator=g) < 0.1] = float("-inf")
+    wide[5], wide[7], wide[11] = float("-inf"), float("nan"), torch.finfo(torch.float16).min
+    wide[9, : E // 2] = float("inf")
+    bias = torch.randn(E, generator=g) * 0.02 if E % 2 else None
+    check_route(wide.cuda()[:, 2:2 + E], bias, (E, k, G, TG, score, gs, T % 2 == 0, 2.5))
