@@ -269,3 +269,50 @@ def test_route_scored_fp16_batches(score, gs, T, E, k, G, TG):
     wide[9, : E // 2] = float("inf")
     bias = torch.randn(E, generator=g) * 0.02 if E % 2 else None
     check_route(wide.cuda()[:, 2:2 + E], bias, (E, k, G, TG, score, gs, T % 2 == 0, 2.5))
+
+
+# --- streams -------------------------------------------------------------------------------------
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_experts_calls_on_a_given_stream(as_handle):
+    """SwiGLU's codes, the experts' product and the combine enqueue on the
+    stream they are given: behind a wait there, nothing is written yet when the
+    current stream looks, and all of it is afterwards."""
+    T, k, E, H, I = 6, 2, 4, 72, 64
+    P = T * k
+    g, u = acts(P, I, torch.bfloat16, 1), acts(P, I, torch.bfloat16, 2)
+    idx = routing(T, k, E, 3)
+    offs, perm = (torch.from_numpy(v).cuda() for v in R.tables(idx.numpy(), E))
+    w, ws = codes(E, H, I, seed=3), scales(E, H)
+    wt, idx = torch.rand(T, k, generator=gen(4)).cuda(), idx.cuda()
+    q, s = torch.full((P, I), 99, dtype=torch.int8, device="cuda"), torch.full((P,), -1.0, device="cuda")
+    o, y = torch.full((P, H), 5.0, device="cuda"), torch.full((T, H), 7.0, device="cuda")
+    st = torch.cuda.Stream()
+    at = st.cuda_stream if as_handle else st
+
+    def run():
+        B.coli_swiglu_quant_token(g, u, q, s, stream=at)
+        B.coli_gemm_q8_grouped(q, s, w.view(torch.uint8), ws, offs, perm, o, stream=at)
+        B.coli_moe_combine(o, idx, wt, y, stream=at)
+        return [t.clone() for t in (q, s, o, y)]  # on the current stream, which does not wait
+
+    run()  # loads the kernels, which takes longer than the wait below
+    torch.cuda.synchronize()
+    for t, v in ((q, 99), (s, -1.0), (o, 5.0), (y, 7.0)):
+        t.fill_(v)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(200_000_000)  # what follows on this stream waits
+    early = run()
+    torch.cuda.current_stream().synchronize()
+    assert not st.query()  # it waits still
+    st.synchronize()
+    assert [t.unique().tolist() for t in early] == [[99], [-1.0], [5.0], [7.0]]
+    rq, rs = R.quant(R.swiglu(f64(g), f64(u)))
+    np.testing.assert_array_equal(q.cpu().numpy(), rq)
+    flat, ref = idx.cpu().numpy().ravel(), np.zeros((P, H))
+    for e in range(E):
+        p = np.flatnonzero(flat == e)
+        ref[p] = R.product(rq[p], rs[p], w[e].cpu().numpy(), ws[e].cpu().numpy())
+    assert_product(o, ref, torch.float32)
+    terms = f64(o).reshape(T, k, H) * f64(wt)[:, :, None]
+    assert (np.abs(f64(y) - terms.sum(1)) <= (k + 1) * 2.0 ** -24 * 1.01 * np.abs(terms).sum(1)).all()
