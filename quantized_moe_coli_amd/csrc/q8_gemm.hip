@@ -458,30 +458,26 @@ struct SweepKernel {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-    // a chunk's products go by groups of GS token operands, the first half of
-    // k first, each read from LDS while the group before is multiplied
-    constexpr int GS = MT % 4 == 0 ? 4 : MT == 10 ? 5 : MT == 6 ? 3 : MT, NG = 2 * MT / GS;
-    static_assert(MT % GS == 0, "whole groups");
-    v4i x[2][GS];
-    auto read = [&](int c, int g) {
-      const int h = g / (MT / GS), j0 = g % (MT / GS) * GS;
+    // a chunk's products go by the halves of its k, each half's token operands
+    // read from LDS while the half before is multiplied
+    v4i x[2][MT];
+    auto read = [&](int c, int h) {
       const unsigned char *buf = ring + (c % (D + 1)) * XB + li * SB + 16 * ((4 * h + lg) ^ key(li));
 #pragma unroll
-      for (int j = 0; j < GS; ++j) x[g & 1][j] = *reinterpret_cast<const v4i *>(buf + 16 * (j0 + j) * SB);
+      for (int j = 0; j < MT; ++j) x[h][j] = *reinterpret_cast<const v4i *>(buf + 16 * j * SB);
     };
-    auto mul = [&](const v4i (*v)[2], int g) {
-      const int h = g / (MT / GS), j0 = g % (MT / GS) * GS;
+    auto mul = [&](const v4i (*v)[2], int h) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < GS; ++j)
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          acc[i][j0 + j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[h][i], x[g & 1][j], acc[i][j0 + j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[h][i], x[h][j], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     };
 
-    // Step c multiplies chunk c, whose first group has been read.  Before its
-    // last group, a barrier: chunk c + 1's codes have landed for every wave,
+    // Step c multiplies chunk c, whose first half has been read.  Before its
+    // second half, a barrier: chunk c + 1's codes have landed for every wave,
     // and every wave has read chunk c's, whose place the codes D + 1 chunks
     // ahead take.  (The loop of whole chunks is entered from straight code:
     // with a branch on the way the compiler would not know how many loads are
@@ -502,15 +498,12 @@ struct SweepKernel {
       do {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-#pragma unroll
-          for (int g = 0; g < NG - 1; ++g) {
-            read(c + u, g + 1);
-            mul(w[u], g);
-          }
+          read(c + u, 1);
+          mul(w[u], 0);
           stage_barrier<(D - 1) * (LX + LW) + LW>();
           read(c + u + 1, 0);
           issue(c + u + 1 + D);
-          mul(w[u], NG - 1);
+          mul(w[u], 1);
           keep_order();
           load(w[u], c + u + D);
           keep_order();
@@ -534,15 +527,12 @@ struct SweepKernel {
 #pragma unroll
       for (int u = 0; u < D; ++u)
         if (c + u < chunks) {
-#pragma unroll
-          for (int g = 0; g < NG - 1; ++g) {
-            read(c + u, g + 1);
-            mul(w[u], g);
-          }
+          read(c + u, 1);
+          mul(w[u], 0);
           stage_barrier<0>();
           if (c + u + 1 < chunks) read(c + u + 1, 0);
           if (c + u + 1 + D < chunks) issue(c + u + 1 + D);
-          mul(w[u], NG - 1);
+          mul(w[u], 1);
           if (c + u + D < full) load(w[u], c + u + D);
           else if (c + u + D < chunks) load_part(w[u], c + u + D);
         }
@@ -616,14 +606,14 @@ struct SweepKernel {
   }
 };
 
-// The smallest of the variants MT = 1, 2, 4, 6, ... MAX that holds n tokens.
+// The smallest of the variants MT = 1, 2, 4, ... MAX that holds n tokens.
 template <int MAX, int M = 1, typename K>
 __device__ __forceinline__ void sweep_dispatch(K &k, int n) {
   if constexpr (M >= MAX) {
     k.template run<MAX>();
   } else {
     if (n <= 16 * M) k.template run<M>();
-    else sweep_dispatch<MAX, M == 1 ? 2 : M + 2>(k, n);
+    else sweep_dispatch<MAX, 2 * M>(k, n);
   }
 }
 
@@ -675,9 +665,10 @@ __global__ __launch_bounds__(64 * NW) void k_q8_sweep(Q8Args a, int nbm, int nbn
 // us at 128 x 147456 x 6144).  Storing rows whole instead of 8 bytes of each
 // took 32 us off.
 // ---------------------------------------------------------------------------
-template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
 struct TileKernel {
   typedef typename Elem<DT>::type T;
+  static constexpr int SB = 128;
   static constexpr int NW = WM * WN;
   static constexpr int TN = BN / WN / 32;       // channel groups of a wave
   static constexpr int TMAX = BM / WM / 32;     // token groups of a wave, at most
@@ -685,7 +676,7 @@ struct TileKernel {
   static constexpr int RPL = 64 / PPR;          // rows of a load
   static constexpr int KSN = SB / 32;           // steps of a stage
   static constexpr int LW = BN / RPL / NW;      // weight loads of a wave in a stage
-  static_assert((SB == 64 || SB == 128 || SB == 256) && BN % (RPL * NW) == 0, "whole loads");
+  static_assert(BN % (RPL * NW) == 0, "whole loads");
   // place of piece p of row r: p ^ key(r); 256 / SB rows span the banks
   __device__ __forceinline__ static int key(int r) { return (r / (256 / SB)) & (PPR - 1); }
 
@@ -830,8 +821,8 @@ struct TileKernel {
     constexpr int EPC = 16 / (int)sizeof(T);        // elements of a 16-byte chunk
     constexpr int CH = 32 * TN / EPC;               // chunks of a row
     // bytes of a row in the area: chunk c of row r lies at c ^ (r % 8)
-    constexpr int ROWB = 16 * (CH <= 8 ? 8 : CH <= 16 ? 16 : 32);
-    static_assert(NW * 32 * ROWB <= LDS, "area");
+    constexpr int ROWB = 16 * (CH <= 8 ? 8 : 16);
+    static_assert(64 % CH == 0 && CH <= 16 && NW * 32 * ROWB <= LDS, "whole rows a store, and the area");
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
     float sn[TN][16], bn[TN][16];
@@ -868,8 +859,7 @@ struct TileKernel {
       if (vec) {
 #pragma unroll
         for (int p = 0; p < 32 * CH / 64; ++p) {
-          const int rr = 64 % CH == 0 ? p * (64 / CH) + lane / CH : (p * 64 + lane) / CH;
-          const int ch = 64 % CH == 0 ? lane % CH : (p * 64 + lane) % CH;
+          const int rr = p * (64 / CH) + lane / CH, ch = lane % CH;
           const Pack<T, EPC> v = *reinterpret_cast<const Pack<T, EPC> *>(area + rr * ROWB + ((ch ^ (rr & 7)) * 16));
           const int n = nw + ch * EPC;
           if (t0 + rr >= t.n || n >= a.N) continue;
@@ -913,7 +903,7 @@ __device__ __forceinline__ void tile_dispatch(K &k, int tm) {
   }
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
 __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, unsigned char *ring, int *rows,
                                           float *chans) {
   Tile t;
@@ -935,34 +925,32 @@ __device__ __forceinline__ void tile_body(const Q8Args &a, int nbm, int nbn, uns
   for (int i = threadIdx.x; i < BN; i += 64 * WM * WN)
     chans[i] = a.ws[(size_t)t.e * a.N + min(t.nb * BN + i, a.N - 1)];
   __syncthreads();
-  TileKernel<DT, BM, BN, WM, WN, SB, LDS, GROUPED> k{a, t, ring, rows, chans};
+  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED> k{a, t, ring, rows, chans};
   tile_dispatch<BM / WM / 32>(k, (t.n + 32 * WM - 1) / (32 * WM));
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int SB, int LDS, bool GROUPED>
+template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
 // (LDS past half a CU's leaves room for one workgroup)
 __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 : 1) void k_q8_tile(Q8Args a, int nbm, int nbn) {
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
   __shared__ float chans[BN];
-  tile_body<DT, BM, BN, WM, WN, SB, LDS, GROUPED>(a, nbm, nbn, ring, rows, chans);
+  tile_body<DT, BM, BN, WM, WN, LDS, GROUPED>(a, nbm, nbn, ring, rows, chans);
 }
 
 // ---------------------------------------------------------------------------
 // The variants and the choice among them.  A variant's tile (bm tokens x bn
-// channels) and threads are its kernel's; `slots` is how many of its
-// workgroups the 256 CUs hold at once.
+// channels) and threads are its kernel's.
 // ---------------------------------------------------------------------------
 enum Variant {
   kRing16x16, kRing16x32, kRing32x64, kRing64x32, kRing64x64, kSweep32, kSweep64,
   kTile128, kTile128Deep, kTile256, kVariants
 };
 struct Shape {
-  int bm, bn, threads, slots;
+  int bm, bn, threads;
 };
-constexpr Shape kShapes[kVariants] = {
-    {16, 16, 256, 512}, {16, 32, 256, 512},   {32, 64, 256, 512},   {64, 32, 512, 512},   {64, 64, 512, 512},
-    {32, 64, 128, 2048}, {64, 128, 256, 768}, {128, 128, 256, 512}, {128, 128, 256, 256}, {256, 256, 512, 256}};
+constexpr Shape kShapes[kVariants] = {{16, 16, 256}, {16, 32, 256},  {32, 64, 256},   {64, 32, 512},   {64, 64, 512},
+                                      {32, 64, 128}, {64, 128, 256}, {128, 128, 256}, {128, 128, 256}, {256, 256, 512}};
 
 // Upper bound of the token tiles of bm over E experts with P pairs.
 int64_t max_tiles(const Q8Args &a, int bm) { return a.P / bm + (a.P < a.E ? a.P : a.E); }
@@ -993,7 +981,7 @@ Variant grouped_variant(const Q8Args &a) {
 
 // The dense product: the variant of the least time, from what each takes at
 // 4096 columns (in 0.1 us) with at most one workgroup a CU, and for a full
-// round of its slots.  Over 1 to 3000 tokens x 300 to 40000 channels x 1024,
+// round of its slots, the workgroups that the 256 CUs hold at once.  Over 1 to 3000 tokens x 300 to 40000 channels x 1024,
 // 2560 and 6144 columns that is the best variant or within 15 % of it but for
 // one of 150 sizes (3000 x 300 x 6144: 64x32 27 us, 64x64 22).  Some of both
 // sides (us, 6144 columns):
@@ -1007,11 +995,11 @@ Variant grouped_variant(const Q8Args &a) {
 Variant dense_variant(const Q8Args &a) {
   struct Time {
     Variant v;
-    int first, round;
+    int slots, first, round;
   };
-  constexpr Time kTimes[] = {{kRing16x16, 58, 70},   {kRing16x32, 67, 82},       {kRing32x64, 108, 140},
-                             {kRing64x32, 83, 138},  {kRing64x64, 140, 185},     {kTile128Deep, 240, 0},
-                             {kTile128, 265, 410},   {kTile256, 565, 693}};
+  constexpr Time kTimes[] = {{kRing16x16, 512, 58, 70},  {kRing16x32, 512, 67, 82},   {kRing32x64, 512, 108, 140},
+                             {kRing64x32, 512, 83, 138}, {kRing64x64, 512, 140, 185}, {kTile128Deep, 256, 240, 0},
+                             {kTile128, 512, 265, 410},  {kTile256, 256, 565, 693}};
   if (a.rows > 32 && a.rows <= 64 && a.N >= 65536) return kSweep64;
   Variant best = kTile256;
   int64_t least = INT64_MAX;
@@ -1019,7 +1007,7 @@ Variant dense_variant(const Q8Args &a) {
     const Shape &s = kShapes[t.v];
     const int64_t n = workgroups(a, t.v);
     if ((s.bm > 16 && s.bm >= 2 * (int64_t)a.rows) || (n > 256 && t.round == 0)) continue;
-    const int64_t cost = n <= 256 ? t.first : t.round * ((n + s.slots - 1) / s.slots);
+    const int64_t cost = n <= 256 ? t.first : t.round * ((n + t.slots - 1) / t.slots);
     if (cost < least) {
       least = cost;
       best = t.v;
@@ -1043,10 +1031,10 @@ void run_sweep(const Q8Args &a, int64_t wgs, hipStream_t st) {
   hipLaunchKernelGGL((k_q8_sweep<DT, BM, NW, D, GROUPED>), dim3(wgs), dim3(64 * NW), 0, st, a, nbm, nbn);
 }
 
-template <int DT, bool GROUPED, int BM, int BN, int WM, int WN, int SB, int LDS>
+template <int DT, bool GROUPED, int BM, int BN, int WM, int WN, int LDS>
 void run_tile(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + BN - 1) / BN, nbm = (a.rows + BM - 1) / BM;
-  hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, SB, LDS, GROUPED>), dim3(wgs), dim3(64 * WM * WN), 0, st,
+  hipLaunchKernelGGL((k_q8_tile<DT, BM, BN, WM, WN, LDS, GROUPED>), dim3(wgs), dim3(64 * WM * WN), 0, st,
                      a, nbm, nbn);
 }
 
@@ -1071,7 +1059,7 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
         case kRing64x32: run_ring<DT, true, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
         case kSweep32: run_sweep<DT, true, 32, 2, 4>(a, wgs, st); break;
         case kSweep64: run_sweep<DT, true, 64, 4, 3>(a, wgs, st); break;
-        default: run_tile<DT, true, 256, 256, 1, 8, 128, 157 << 10>(a, wgs, st); break;
+        default: run_tile<DT, true, 256, 256, 1, 8, 157 << 10>(a, wgs, st); break;
       }
     } else {
       switch (v) {
@@ -1081,9 +1069,9 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st) {
         case kRing64x32: run_ring<DT, false, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
         case kRing64x64: run_ring<DT, false, 64, 64, 2, 2, 2, 2>(a, wgs, st); break;
         case kSweep64: run_sweep<DT, false, 64, 4, 3>(a, wgs, st); break;
-        case kTile128: run_tile<DT, false, 128, 128, 2, 2, 128, 64 << 10>(a, wgs, st); break;
-        case kTile128Deep: run_tile<DT, false, 128, 128, 2, 2, 128, 128 << 10>(a, wgs, st); break;
-        default: run_tile<DT, false, 256, 256, 2, 4, 128, 144 << 10>(a, wgs, st); break;
+        case kTile128: run_tile<DT, false, 128, 128, 2, 2, 64 << 10>(a, wgs, st); break;
+        case kTile128Deep: run_tile<DT, false, 128, 128, 2, 2, 128 << 10>(a, wgs, st); break;
+        default: run_tile<DT, false, 256, 256, 2, 4, 144 << 10>(a, wgs, st); break;
       }
     }
     return hipGetLastError();
