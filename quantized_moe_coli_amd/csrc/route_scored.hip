@@ -343,11 +343,15 @@ hipError_t launch_route_scored(int dt, const ScoreCfg &c, const void *logits, in
   while (gp < c.n_group) gp *= 2;
   const int L = 64 / gp;
   const int need = (c.E / c.n_group + L - 1) / L;  // at most 32: E <= 1024, gp < 2 n_group
-  // four tokens a wave from 1024 tokens on (16384 x 256: 17.8 us, by a wave each 23.4), where 16 lanes
-  // hold a token's experts in 16 registers each
+  // Four tokens a wave where they fill the chip and 16 lanes hold a token's experts in 16 registers each
+  // (us, a wave for each token / four tokens a wave):
+  //   256 experts, softmax, bf16:    1024 tokens 5.2 / 9.2, 4096 8.1 / 9.5, 8192 12.8 / 11.0, 16384 21.7 / 16.6
+  //   256 in 8 groups, sigmoid, f32: 1024 tokens 5.5 / 10.2, 4096 8.3 / 10.2, 8192 12.8 / 13.8, 16384 22.4 / 20.4
+  //   128 experts, softmax, bf16:    1024 tokens 3.6 / 5.3, 4096 4.9 / 5.4, 8192 7.2 / 6.1, 16384 11.8 / 8.4
+  //   64 experts, softmax, bf16:     1024 tokens 4.1 / 5.1, 3000 4.9 / 5.1, 4096 5.5 / 5.1, 16384 13.6 / 7.4
   const int L16 = gp <= kRowLanes ? kRowLanes / gp : 0;
   const int need16 = L16 ? (c.E / c.n_group + L16 - 1) / L16 : 99;
-  const bool rows = T >= 1024 && need16 <= 16 && c.k <= kRowK;
+  const bool rows = T >= (need16 <= 4 ? 4096 : 8192) && need16 <= 16 && c.k <= kRowK;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     const auto *lg = static_cast<const typename Elem<DT>::type *>(logits);

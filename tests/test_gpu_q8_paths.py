@@ -316,3 +316,43 @@ def test_experts_calls_on_a_given_stream(as_handle):
     assert_product(o, ref, torch.float32)
     terms = f64(o).reshape(T, k, H) * f64(wt)[:, :, None]
     assert (np.abs(f64(y) - terms.sum(1)) <= (k + 1) * 2.0 ** -24 * 1.01 * np.abs(terms).sum(1)).all()
+
+
+# --- four tokens a wave --------------------------------------------------------------------------
+@pytest.mark.parametrize("dt,score,gs", [("f32", "softmax", "max"), ("bf16", "sigmoid", "top2"),
+                                         ("f16", "softmax", "top2")])
+@pytest.mark.parametrize("T,E,k,G,TG", [(8192, 256, 8, 1, 1), (8195, 256, 16, 8, 4), (4096, 60, 6, 4, 2),
+                                        (4099, 16, 9, 16, 9), (8193, 45, 5, 9, 3), (4101, 7, 3, 1, 1),
+                                        (8194, 128, 4, 2, 1), (8191, 256, 8, 1, 1), (4095, 64, 8, 1, 1),
+                                        (8200, 256, 17, 1, 1), (8197, 512, 8, 8, 3)])
+def test_route_scored_four_tokens_a_wave(dt, score, gs, T, E, k, G, TG):
+    """Batches from which four tokens share a wave, and neighbours of that
+    limit.  Some rows of each kind against the definition; every row against
+    the same rows in small batches, which a wave each routes: equal indices,
+    and weights whose scores may round differently (by one step, where the two
+    orders of a binary64 sum lie on both sides of a border: two half-steps for
+    the score and for the sum's, and the quotient's half-step on each side)."""
+    g = gen(T, E, k)
+    logits = torch.randn(T, E, generator=g) * 2
+    logits[::3] = torch.randint(-3, 4, (len(range(0, T, 3)), E), generator=g).float()
+    logits[torch.rand(T, E, generator=g) < 0.1] = float("-inf")
+    logits[5], logits[7], logits[11] = float("-inf"), float("nan"), torch.finfo(torch.bfloat16).min
+    logits[9, : E // 2] = float("inf")
+    bias = (torch.randn(E, generator=g) * 0.02).cuda() if E % 2 else None
+    lg = logits.to(DT[dt]).cuda()
+    norm = T % 2 == 0
+    cfg = B.score_cfg(E, k, G, TG, score=B.SCORE_SOFTMAX if score == "softmax" else B.SCORE_SIGMOID,
+                      group_score=B.GROUP_TOP2 if gs == "top2" else B.GROUP_MAX, norm_topk_prob=int(norm),
+                      routed_scaling_factor=2.5)
+    idx, w = torch.full((T, k), 12345, dtype=torch.int32, device="cuda"), torch.full((T, k), 9.0, device="cuda")
+    B.coli_moe_route_scored(cfg, lg, bias, idx, w)
+    si, sw = torch.empty_like(idx), torch.empty_like(w)
+    for a in range(0, T, 1000):
+        B.coli_moe_route_scored(cfg, lg[a:a + 1000], bias, si[a:a + 1000], sw[a:a + 1000])
+    assert torch.equal(idx, si)
+    assert ((w - sw).abs().double() <= 6 * 2.0 ** -24 * sw.abs().double()).all()
+    some = torch.cat([torch.arange(40), torch.randint(0, T, (150,), generator=g), torch.arange(T - 20, T)]).cuda()
+    ri, rw = R.route(lg[some].float().cpu().numpy(), None if bias is None else bias.cpu().numpy(), k, G, TG, score,
+                     gs, norm, 2.5)
+    np.testing.assert_array_equal(idx[some].cpu().numpy(), ri)
+    assert (np.abs(f64(w[some]) - rw) <= (k + 3) * 2.0 ** -24 * np.abs(rw) + 2.0 ** -149).all()
