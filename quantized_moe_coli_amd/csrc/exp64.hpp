@@ -1,7 +1,8 @@
 // exp64.hpp -- an exponential and a reciprocal in binary64, exact enough to be
-// rounded to binary32 afterwards (about 2^-47 of the value; a rounding to
-// binary32 is then that of the exact value but for one case in 2^22), in
-// about half the instructions of the math library's.
+// rounded to binary32 afterwards (off by at most 2^-46.6 of the value; a
+// rounding to binary32 is then that of the exact value but for one case in
+// 2^21.6 where the error is largest, and goes to the other neighbour there),
+// in about half the instructions of the math library's.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,7 +10,8 @@
 namespace coli {
 
 // exp(x): x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor series of e^r
-// up to r^11 (the rest is below 2^-47 of the result).  Past +-1100 it is 0 or
+// up to r^11 (the rest, r^12 / 12! and smaller terms, is below 2^-46.6 of the
+// result: most at r = -ln 2 / 2, where it is 2^-46.7).  Past +-1100 it is 0 or
 // infinity, whatever x.
 __device__ __forceinline__ double exp_64(double x) {
   x = __builtin_fmin(__builtin_fmax(x, -1100.0), 1100.0);

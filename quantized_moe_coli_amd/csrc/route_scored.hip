@@ -6,8 +6,9 @@
 // 64 / (groups rounded up to a power of two) lanes each, so that a group's
 // best scores are found by a reduction over L neighbouring lanes; lane l of
 // a group holds its experts l, l + L, ...  The scores are evaluated in
-// binary64 and rounded once to binary32, so neither the order of a sum nor
-// the approximation of an exponential moves an expert past another.
+// binary64 and rounded once to binary32, so the order of a sum and the
+// approximation of an exponential change a score only where it lies next to a
+// border of that rounding (about one in four million), and then by one step.
 //
 // Bound by instructions, not by memory: a token's exponentials and the k
 // rounds of its selection.  Reductions go by DPP moves instead of the LDS
