@@ -174,10 +174,11 @@ __device__ __forceinline__ void stage_barrier() {
 //
 // Loads of whole 256-byte runs of rows are what this kernel is about: read
 // straight into operand registers (64 bytes of 16 rows an instruction) the
-// tokens' codes cost more than the weights from 16 tokens on (6144 x 6144,
-// one launch after another: 1 token 9.1 us against 7.3 here, 16 tokens 10.4
-// against 7.6, 61 tokens 18.8 against 10.1).  Bound by latency at such sizes:
-// 37.7 MB of weights alone would take 6.3 us.
+// tokens' codes cost more than the weights from 16 tokens on (1.25 times as
+// long at 1 token of 6144 x 6144, 1.4 at 16, 1.9 at 61).  6144 x 6144, launches
+// one after another, with 18 matrices in turn, which come from memory: 1 token
+// 9.9 us, 16 tokens 10.7, 61 tokens 15.6; with one, which stays in the Infinity
+// Cache: 9.2, 9.7, 11.6.  Bound by latency: 37.7 MB from memory take 6.3 us.
 //
 // LDS: a row's stage is 16 pieces of 16 bytes, piece p of row r at place p ^
 // (r % 16): 16 lanes that read 16 rows at one k meet all 64 banks.
@@ -373,10 +374,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(Q8Args a, int nbm
 // The products are 16 x 16 x 64, MT groups of 16 tokens (as many as the tile
 // has tokens for) by two of 16 channels for each wave.
 //
-// Bound by the memory: 24 experts of 4096 x 6144 with a token each 104 us, 5.8
-// TB/s (a plain read reaches 6.0); 64 experts of 6144 x 2048 with 31 tokens 165
-// us, 4.9 TB/s.  Workgroups of few waves, several to a CU, hide one another's
-// start and end (eight waves with 64 tokens: 193 us).
+// Bound by the memory: 24 experts of 4096 x 6144 with a token each 104-109 us,
+// 5.5-5.8 TB/s (a plain read reaches 6.0); 64 experts of 6144 x 2048 with 31
+// tokens 162-171 us, 4.7-5.0 TB/s.  Workgroups of few waves, several to a CU,
+// hide one another's start and end (eight waves with 64 tokens take 1.17 times
+// as long).
 // ---------------------------------------------------------------------------
 template <int DT, int BM, int NW, int D, bool GROUPED>
 struct SweepKernel {
@@ -658,12 +660,12 @@ __global__ __launch_bounds__(64 * NW) void k_q8_sweep(Q8Args a, int nbm, int nbn
 // read.  Rows past the tile and pieces past the row's end read valid
 // addresses near them; what they bring in is never used.
 //
-// 8192 x 6144 x 6144 to bfloat16: 290 us, 2.13 POPS, where the library's int8
-// product reaches 2.19.  What bounds it is power: on zeros the same launch
-// takes 220 us; other wave shapes and operands two steps ahead change nothing,
-// and stages of 64 bytes, which ask for each line twice, cost (276 against 225
-// us at 128 x 147456 x 6144).  Storing rows whole instead of 8 bytes of each
-// took 32 us off.
+// 8192 x 6144 x 6144 to bfloat16: 282-293 us, 2.11-2.19 POPS, where the
+// library's int8 product reaches 2.19.  What bounds it is power: on zeros the
+// same launch takes 220 us; other wave shapes and operands two steps ahead
+// change nothing, and stages of 64 bytes, which ask for each line twice, cost
+// (1.23 times as long at 128 x 147456 x 6144).  Storing rows whole instead of 8
+// bytes of each took 32 us off.
 // ---------------------------------------------------------------------------
 template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED>
 struct TileKernel {
@@ -962,15 +964,27 @@ int64_t workgroups(const Q8Args &a, Variant v) {
   return (nbm * nbn + 7) / 8 * 8;
 }
 
-// Experts' products, by the tokens of an expert on average.  The sweep reads
-// each weight once at the rate of the memory as long as its workgroups fill
-// the chip; the rings split k and fill it with fewer channels.  64 experts of
-// 6144 x 2048: 10 tokens each 148 us by kSweep32 (ring 163), 31 tokens 165 us
-// by kSweep64 (ring 208); 256 experts of 4096 x 6144: 64 tokens 1370 us by
-// kTile256 (a sweep of up to 192 tokens 1436), 128 tokens 1493 (1613).
+// Experts' products, by the tokens of an expert on average (P / E: what the
+// host knows; dropped slots count too).  The sweep reads each weight once at
+// the rate of the memory as long as its workgroups fill the chip; the rings
+// split k and fill it with fewer channels.  In us, launches one after another:
+//   64 experts of 6144 x 2048:   16x32, 64x32, sweeps of 32, 64, tile
+//     10 tokens each             152,   254,   149,   150,   149
+//     31                         219,   268,   168,   162,   161
+//     50                         332,   292,   234,   176,   173
+//   256 experts of 4096 x 6144:
+//     10                         1105,  1694,  1106,  1095,  1070
+//     64, 128                    sweep of 64 1345, 1983; tile 1212, 1409
+//   24 experts of 4096 x 6144:
+//     1                          107,   172,   115,   116,   123
 // (The experts' kTile256 gives each wave 32 channels of all tokens: cost
-// follows the tokens by 32, and three stages fit up to 160 tokens; by 2 x 4
-// waves as in the dense product 1544 us.)
+// follows the tokens by 32, and three stages fit up to 160 tokens; 2 x 4 waves
+// as in the dense product take 1.03 times as long at 128 tokens.)
+// Uneven routing: where the tokens go with 1 / rank over 64 or 256 experts, the
+// choice is within 6 % of the best (8192 pairs over 256 experts: 1332, tile
+// 1257), and with half of them in one expert 4 % (512: 1060, 16x32 1023).  It
+// costs where few experts take all of a batch that would fill many: 8 of 256
+// experts with 256 tokens each 216 us by kSweep32, 83 by the tile.
 Variant grouped_variant(const Q8Args &a) {
   const int64_t avg = ((int64_t)a.P + a.E - 1) / a.E;
   const int64_t used = a.P < a.E ? a.P : a.E;  // experts with a token, at most
@@ -981,17 +995,25 @@ Variant grouped_variant(const Q8Args &a) {
 
 // The dense product: the variant of the least time, from what each takes at
 // 4096 columns (in 0.1 us) with at most one workgroup a CU, and for a full
-// round of its slots, the workgroups that the 256 CUs hold at once.  Over 1 to 3000 tokens x 300 to 40000 channels x 1024,
-// 2560 and 6144 columns that is the best variant or within 15 % of it but for
-// one of 150 sizes (3000 x 300 x 6144: 64x32 27 us, 64x64 22).  Some of both
-// sides (us, 6144 columns):
-//   30 x 2048   16x16 7.7, 64x32 10.6              1 x 6144     16x32 9.1, 64x32 11.0
-//   61 x 6144   64x32 12.0, 16x32 17.6             200 x 6144   64x64 22.4, 64x32 26.0
-//   509 x 6144  128x128 of one a CU 33.6,          1500 x 6144  256x256 80.6, 128x128 85.4
-//               of two 37.8, 64x64 40.8            3000 x 6144  128x128 134.6, 256x256 160.6
-// (Blocks whose tokens would be half empty are left out.)  With very many
-// channels all are bound by the memory: 61 x 131072 channels of 6144 columns 160
-// us by the sweep, 177 by 64x64.
+// round of its slots, the workgroups that the 256 CUs hold at once.  The table
+// was made with one matrix again and again, of which the Infinity Cache keeps
+// up to 256 MB; a model goes on to its next matrix.  Measured so, with matrices
+// of 640 MB together in turn (64 at most), over 1 to 3000 tokens x 300 to 40000
+// channels x 1024, 2560 and 6144 columns, the choice is the best variant or
+// within 15 % of it at 270 of 273 sizes (3000 x 300 x 6144: 64x32 26.9 us,
+// 32x64 20.2; x 2560 13.2, 11.0; 61 x 40000 x 1024: 64x64 17.7, 128x128 15.4).
+// Some of both sides (us, 6144 columns, matrices in turn):
+//   30 x 2048   16x16 8.4, 64x32 12.7              1 x 6144     16x32 9.9, 64x32 13.6
+//   61 x 6144   64x32 15.6, 16x32 20.5             200 x 6144   64x64 27.3, 64x32 27.9
+//   509 x 6144  128x128 of one a CU 34.7,          1500 x 6144  256x256 78.1, 128x128 87.7
+//               of two 47.8, 64x64 54.6            3000 x 6144  128x128 137.4, 256x256 159.1
+// (Blocks whose tokens would be half empty are left out.)  33 to 64 tokens of
+// very many channels are bound by the memory in every form: the sweep is within
+// 11 % of the best, 128x128 within 9 %, 64x64 within 24 %, 64x32 within 36 %
+// (us, sweep / 64x64 / 128x128 / 64x32): 61 x 65536 x 6144 91 / 88 / 83 / 106, 48 x 65536 x 2048 31 / 33 / 30
+// / 39, 61 x 131072 x 6144 172 / 168 / 158 / 205, 48 x 151936 x 2048 70 / 78 / 76
+// / 86, 61 x 151936 x 1024 41 / 51 / 44 / 56.  Below 65536 channels it is not:
+// 64 x 32768 x 6144 53 / 44 / 58 / 56.
 Variant dense_variant(const Q8Args &a) {
   struct Time {
     Variant v;

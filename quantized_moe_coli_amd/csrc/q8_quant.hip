@@ -19,9 +19,10 @@
 // was approximated moves h by one step in about one case in four million, and
 // a code only where its quotient lies next to a half then.
 //
-// 8192 x 6144 bfloat16 30 us (150 MB, 5.0 TB/s: what a copy reaches); SwiGLU of
-// 32768 x 2048 99 us (335 MB), bound by the binary64 instructions of its
-// exponential; the sum of 4096 x 8 rows of 6144 85 us (453 MB, 5.3 TB/s).
+// 8192 x 6144 bfloat16 30-32 us (150 MB, 4.7-5.0 TB/s: what a copy reaches);
+// SwiGLU of 32768 x 2048 96-111 us (335 MB), bound by the binary64 instructions
+// of its exponential; the sum of 4096 x 8 rows of 6144 to bfloat16 85 us from
+// bfloat16 rows (453 MB, 5.3 TB/s), 170 us from fp32 rows (856 MB, 5.0 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -221,7 +222,11 @@ hipError_t launch_quant_token(int dt, const void *x, int64_t ldx, const void *u,
     };
     auto by_len = [&](auto glu, auto vecc) {
       // few rows: as many threads as a row has pieces, which is the shortest way
-      // through it (8 rows of 2048, SwiGLU: 4.1 us, by 64 threads a row 6.7)
+      // through it (us, by pieces / by 4 pieces a thread; bfloat16):
+      //   2048 columns:          8 rows 2.8 / 4.0, 512 rows 3.1 / 4.5, 1024 3.5 / 4.8, 4096 7.2 / 6.8
+      //   2048 columns, SwiGLU:  8 rows 3.2 / 5.9, 512 rows 4.2 / 6.4, 1024 5.7 / 6.5, 4096 16.0 / 16.0
+      //   6144 columns:          8 rows 3.0 / 3.7, 512 rows 4.5 / 4.6, 1024 7.0 / 5.8, 4096 20.5 / 16.4
+      //   6144 columns, SwiGLU:  8 rows 4.5 / 5.1, 512 rows 8.2 / 7.8, 1024 14.4 / 12.4, 4096 52.1 / 39.8
       const int few = T <= 512 ? kPieces : 1;
       if (n * few <= 64 * kPieces * kPiece) go(glu, vecc, std::integral_constant<int, 64>());
       else if (n * few <= 256 * kPieces * kPiece) go(glu, vecc, std::integral_constant<int, 256>());
