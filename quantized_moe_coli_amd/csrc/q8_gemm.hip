@@ -1008,12 +1008,14 @@ Variant grouped_variant(const Q8Args &a) {
 //   509 x 6144  128x128 of one a CU 34.7,          1500 x 6144  256x256 78.1, 128x128 87.7
 //               of two 47.8, 64x64 54.6            3000 x 6144  128x128 137.4, 256x256 159.1
 // (Blocks whose tokens would be half empty are left out.)  33 to 64 tokens of
-// very many channels are bound by the memory in every form: the sweep is within
-// 11 % of the best, 128x128 within 9 %, 64x64 within 24 %, 64x32 within 36 %
-// (us, sweep / 64x64 / 128x128 / 64x32): 61 x 65536 x 6144 91 / 88 / 83 / 106, 48 x 65536 x 2048 31 / 33 / 30
-// / 39, 61 x 131072 x 6144 172 / 168 / 158 / 205, 48 x 151936 x 2048 70 / 78 / 76
-// / 86, 61 x 151936 x 1024 41 / 51 / 44 / 56.  Below 65536 channels it is not:
-// 64 x 32768 x 6144 53 / 44 / 58 / 56.
+// very many channels are bound by the memory in every form; from 65536 channels
+// on neither the sweep nor 128x128 is always the better (us, sweep / 128x128 /
+// 64x64 / 64x32): 61 x 65536 x 1024 20 / 18 / 23 / 28, 48 x 65536 x 6144 88 / 81 /
+// 83 / 99, 61 x 100000 x 6144 159 / 137 / 146 / 162, 48 x 100000 x 4096 106 / 102
+// / 106 / 106, 61 x 150000 x 1024 41 / 44 / 51 / 56, 48 x 150000 x 4096 136 / 150 /
+// 144 / 154.  Over 33, 48 and 61 tokens x 1024 to 6144 columns the sweep is within
+// 16 % of the best of the four, 128x128 13 %, 64x64 28 %, 64x32 54 %.  With fewer
+// channels it is not: 64 x 32768 x 6144 53 / 58 / 44 / 56.
 Variant dense_variant(const Q8Args &a) {
   struct Time {
     Variant v;
