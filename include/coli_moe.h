@@ -388,7 +388,8 @@ coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T,
  * up), fan = 1 one row per (token, slot) pair (down).  q holds `rows` rows,
  * y P rows.  Rows of y that no position names are left as they are.  Positions
  * past P, and pairs outside [0, P) or whose row of q is past `rows`, are
- * skipped.  1 <= E <= 1024, 0 <= P <= 2^25, fan >= 1; the rest as for
+ * skipped: a fan of 1 with one row per token (rows * fan < P) leaves the rows
+ * of y from rows * fan on unwritten, without an error.  1 <= E <= 1024, 0 <= P <= 2^25, fan >= 1; the rest as for
  * coli_gemm_q8.  rows * K of 2^32 or more returns COLI_ERR_UNSUPPORTED. */
 coli_status coli_gemm_q8_grouped(const int8_t *q, const float *s, int32_t rows,
                                  const uint8_t *w, const float *ws, int32_t E,

@@ -418,7 +418,9 @@ def coli_gemm_q8_grouped(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: 
     """The experts' products over coli_moe_dispatch's tables: q int8 [R, K], s
     fp32 [R], w uint8 [E, N, K], ws fp32 [E, N], offs int32 [E + 1], perm int32
     [P] -> row p of y [P, N] = row p // fan of q times p's expert's weights.
-    Rows of pairs that no expert has are left as they are."""
+    fan is the experts per token where q has a row for each token, 1 where it
+    has one for each pair.  Rows of y are left as they are where no expert has
+    the pair, and where q has no row p // fan (R * fan < P)."""
     dev = _device_of(q, "q")
     R, K = q.shape
     E, N = w.shape[0], w.shape[1]
