@@ -367,6 +367,26 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
                                     int32_t n, int8_t *q, float *s,
                                     void *stream);
 
+/* The residual's addition, the root-mean-square norm of the sum, and the norm's
+ * codes, in one pass.  With h = x + res (res [T][n] or NULL: h = x) as one fp32
+ * sum, r_t = 1 / sqrt(mean(h_t^2) + eps) and gain [n] fp32 (NULL: 1), y = h * r *
+ * gain is evaluated in fp64 and rounded once to fp32; h and y are rounded from
+ * fp32 to dtype.  h_out [T][n] receives h, y_out [T][n] y, and q [T][n] (int8,
+ * contiguous, 16-byte aligned) with s [T] the codes of the fp32 y, as
+ * coli_quant_act_token makes them (so their operand is not y as it was rounded to
+ * a 16-bit type).  Each output may be NULL: q and s together, and one of y_out
+ * and q must be there.  h_out and y_out may be x or res themselves, with the same
+ * row stride, but not one another.  A row holding a NaN or an infinity gets NaN
+ * where it stands in y, s = NaN and q = 0.  eps finite and above 0; n at least 1 and
+ * at most 131072, with q a multiple of 32 and at most 131040; 0 <= T <= 2^25 (a row
+ * may be one head's). */
+coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx,
+                                     const void *res, int64_t ldres,
+                                     const float *gain, float eps, int32_t T,
+                                     int32_t n, void *h_out, int64_t ldh,
+                                     void *y_out, int64_t ldy, int8_t *q,
+                                     float *s, void *stream);
+
 /* y [T][N] = s_t * ws_n * sum_k q[t][k] * w[n][k] (+ bias_n), row stride ldy.
  * q [T][K] and s [T] as coli_quant_act_token gives them, w [N][K] and ws [N]
  * an int8 container (coli_quant_pack with COLI_Q8), bias [N] or NULL.  The

@@ -151,6 +151,8 @@ def _load(path: str) -> ctypes.CDLL:
     sig.update({
         "coli_quant_act_token": ([i32, _P, i64, i32, i32, _P, _P, _P], ctypes.c_int),
         "coli_swiglu_quant_token": ([i32, _P, i64, _P, i64, i32, i32, _P, _P, _P], ctypes.c_int),
+        "coli_rmsnorm_quant_token": ([i32, _P, i64, _P, i64, _P, ctypes.c_float, i32, i32, _P, i64,
+                                      _P, i64, _P, _P, _P], ctypes.c_int),
         "coli_gemm_q8": ([_P, _P, i32, _P, _P, i32, i32, _P, i32, _P, i64, _P], ctypes.c_int),
         "coli_gemm_q8_grouped": ([_P, _P, i32, _P, _P, i32, i32, i32, _P, _P, i32, i32, i32, _P,
                                   i64, _P], ctypes.c_int),
@@ -394,6 +396,28 @@ def coli_swiglu_quant_token(g: torch.Tensor, u: torch.Tensor, q: torch.Tensor, s
     _check("coli_swiglu_quant_token", lib().coli_swiglu_quant_token(
         dt, gp, ldg, up, ldu, T, n, _dense(q, torch.int8, T * n, dev, "q"),
         _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream, dev)))
+
+
+def coli_rmsnorm_quant_token(x: torch.Tensor, gain: torch.Tensor | None, eps: float,
+                             q: torch.Tensor | None = None, s: torch.Tensor | None = None,
+                             y: torch.Tensor | None = None, res: torch.Tensor | None = None,
+                             h: torch.Tensor | None = None, stream=None) -> None:
+    """x and res [T, n] (one float type, rows may be strided; res may be None),
+    gain fp32 [n] or None -> those of h [T, n] = x + res, y [T, n] = h * gain /
+    sqrt(mean(h^2) + eps) (of x's type, rows may be strided) and q int8 [T, n], s
+    fp32 [T] (y's codes) that are given.  h and y may be x or res themselves."""
+    dev = _device_of(x, "x")
+    T, n = x.shape
+    dt = _float_type(x, "x")
+    xp, ldx = _rowed(x, T, n, x.dtype, dev, "x")
+    rp, ldr = (None, 0) if res is None else _rowed(res, T, n, x.dtype, dev, "res")
+    hp, ldh = (None, 0) if h is None else _rowed(h, T, n, x.dtype, dev, "h")
+    yp, ldy = (None, 0) if y is None else _rowed(y, T, n, x.dtype, dev, "y")
+    _check("coli_rmsnorm_quant_token", lib().coli_rmsnorm_quant_token(
+        dt, xp, ldx, rp, ldr, None if gain is None else _dense(gain, torch.float32, n, dev, "gain"),
+        eps, T, n, hp, ldh, yp, ldy,
+        None if q is None else _dense(q, torch.int8, T * n, dev, "q"),
+        None if s is None else _dense(s, torch.float32, T, dev, "s"), _raw_stream(stream, dev)))
 
 
 def coli_gemm_q8(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 #include <algorithm>
 #include <map>
@@ -19,6 +20,7 @@ namespace {
 constexpr int kMaxDim = 8192;
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxPairs = 1 << 25;   // kMaxTokens tokens of 32 experts
+constexpr int kMaxNormCols = 1 << 17;
 constexpr int kMaxQ8Cols = 131040;   // 128 * 128 * K < 2^31: the int32 sums are exact
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -434,6 +436,28 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg, c
     if (st != COLI_OK) return st;
     return from_hip(coli::launch_quant_token(dtype, g, ldg, u, ldu, T, n, q, s,
                                              static_cast<hipStream_t>(stream)));
+  });
+}
+
+coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx, const void *res,
+                                     int64_t ldres, const float *gain, float eps, int32_t T, int32_t n,
+                                     void *h, int64_t ldh, void *y, int64_t ldy, int8_t *q, float *s,
+                                     void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxPairs || n <= 0 || n > kMaxNormCols ||
+        !(eps > 0.f && eps <= FLT_MAX))
+      return COLI_ERR_INVALID_ARG;
+    if (q && (n % 32 || n > kMaxQ8Cols)) return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if ((!y && !q) || !q != !s || (y && y == h) || !rows_ok(dtype, x, ldx, n) ||
+        (res && !rows_ok(dtype, res, ldres, n)) ||
+        (h && !rows_ok(dtype, h, ldh, n)) || (y && !rows_ok(dtype, y, ldy, n)) || !aligned(gain, 4) ||
+        !aligned(q, 16) || !aligned(s, 4))
+      return COLI_ERR_INVALID_ARG;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    const coli::NormArgs a{x, res, ldx, ldres, gain, eps, T, n, h, y, ldh, ldy, q, s};
+    return from_hip(coli::launch_norm_quant(dtype, a, static_cast<hipStream_t>(stream)));
   });
 }
 

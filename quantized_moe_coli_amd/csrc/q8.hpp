@@ -1,6 +1,6 @@
 // q8.hpp -- shared by the kernels of the 8-bit products with one scale per
-// token and one per output channel (q8_quant.hip, q8_gemm.hip) and by the
-// scored router (route_scored.hip): element types, and the launchers that
+// token and one per output channel (q8_quant.hip, norm_quant.hip, q8_gemm.hip)
+// and by the scored router (route_scored.hip): element types, and the launchers that
 // the C-ABI layer (api.hip) calls after checking every argument.
 #pragma once
 
@@ -41,6 +41,21 @@ inline hipError_t by_dtype(int dt, F &&fn) {
 // Per-token quantisation of x [T][n] (u null), or of silu(x) * u.
 hipError_t launch_quant_token(int dt, const void *x, int64_t ldx, const void *u, int64_t ldu, int T,
                               int n, int8_t *q, float *s, hipStream_t st);
+
+// h = x + res, its root-mean-square norm y, and y's codes; res, gain, h, y, and
+// q with s may be null.
+struct NormArgs {
+  const void *x, *res;  // [T][n], row strides ldx, ldres
+  int64_t ldx, ldres;
+  const float *gain;    // [n]
+  float eps;
+  int T, n;
+  void *h, *y;          // [T][n], row strides ldh, ldy
+  int64_t ldh, ldy;
+  int8_t *q;            // [T][n]
+  float *s;             // [T]
+};
+hipError_t launch_norm_quant(int dt, const NormArgs &a, hipStream_t st);
 
 // y[t] = (add ? add[t] : 0) + sum_j w[t][j] * o[t * k + j]; o of type odt, which
 // is dt or COLI_F32.

@@ -29,15 +29,14 @@
 
 #include "exp64.hpp"
 #include "q8.hpp"
+#include "token_codes.hpp"
 
 #pragma clang fp contract(off)
 
 namespace coli {
 namespace {
 
-constexpr int kPiece = 8;    // elements per load
 constexpr int kPieces = 4;   // pieces a thread keeps in registers
-constexpr int kGridX = 1 << 20;  // workgroups along x (a launch's threads along one axis fit 32 bits)
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
   const double gd = (double)g;
@@ -59,25 +58,6 @@ __device__ __forceinline__ void load_piece(const typename Elem<DT>::type *p, flo
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) v[j] = (float)p[j];
   }
-}
-
-// Codes of one piece, with the row's scale and its reciprocal.  x * inv
-// differs from the correctly rounded x / s by less than 127 * 2^-22, so
-// rounding it to a whole number gives the same code unless it lies within
-// that of a half; there, and for scales too small for a reciprocal (inv =
-// 0), the division is made.
-__device__ __forceinline__ void codes(const float *v, float s, float inv, uint32_t *out) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < kPiece; ++j) {
-    float r = v[j] * inv;
-    float c = rintf(r);
-    if (fabsf(r - c) > 0.4999f || inv == 0.f) c = rintf(v[j] / s);
-    c = fminf(fmaxf(c, -127.f), 127.f);
-    w[j >> 2] |= ((uint32_t)(int32_t)c & 0xFFu) << (8 * (j & 3));
-  }
-  out[0] = w[0];
-  out[1] = w[1];
 }
 
 // A row by TR threads (64, 256 or 1024), in workgroups of at least 256.  Rows of up to kPieces * TR pieces are read once
@@ -194,12 +174,6 @@ __global__ __launch_bounds__(256) void k_combine_rows(
 #pragma unroll
   for (int i = 0; i < N; ++i) r.v[i] = (T)acc[i];
   *reinterpret_cast<Pack<T, N> *>(y + (int64_t)t * ldy + h) = r;
-}
-
-template <int DT>
-bool rows_aligned(const void *p, int64_t ld, size_t bytes) {
-  return reinterpret_cast<uintptr_t>(p) % bytes == 0 &&
-         (uint64_t)ld * sizeof(typename Elem<DT>::type) % bytes == 0;
 }
 
 }  // namespace
