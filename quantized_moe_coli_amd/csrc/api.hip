@@ -456,7 +456,7 @@ coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx, 
       return COLI_ERR_INVALID_ARG;
     const coli_status st = check_device();
     if (st != COLI_OK) return st;
-    const coli::NormArgs a{x, res, ldx, ldres, gain, eps, T, n, h, y, ldh, ldy, q, s};
+    const coli::NormArgs a{x, res, ldx, ldres, gain, eps, T, n, 1.0 / n, h, y, ldh, ldy, q, s};
     return from_hip(coli::launch_norm_quant(dtype, a, static_cast<hipStream_t>(stream)));
   });
 }

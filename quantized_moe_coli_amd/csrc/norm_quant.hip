@@ -72,6 +72,14 @@ struct Piece {
   }
 };
 
+// 1 / sqrt(v) of a positive v: the instruction's estimate and one step of third
+// order, to a few units of binary64's last place; 0 of an infinity, NaN of NaN.
+__device__ __forceinline__ double inverse_root(double v) {
+  const double r = __builtin_amdgcn_rsq(v);
+  const double e = fma(-v * r, r, 1.0);
+  return r == 0.0 ? 0.0 : fma(r * e, fma(e, 0.375, 0.5), r);
+}
+
 // A row by TR threads (16, 64, 256 or 1024), in workgroups of at least 256.
 // Its first NP * TR pieces are read once and held as h, then as y.
 template <int DT, bool VEC, int TR, int NP>
@@ -110,29 +118,38 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_norm_quant(NormArgs a) 
     }
   };
 
+  // (the pieces that no thread has are passed over by the whole workgroup)
+  auto any = [&](int i) { return i == 0 || i * TR * kPiece < n; };
   float v[NP][kPiece], g0[kPiece];
   {
     P px[NP], pr[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) px[i].template load<TR>(x, i, tr, n);
+    for (int i = 0; i < NP; ++i)
+      if (any(i)) px[i].template load<TR>(x, i, tr, n);
     if (res) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) pr[i].template load<TR>(res, i, tr, n);
+      for (int i = 0; i < NP; ++i)
+        if (any(i)) pr[i].template load<TR>(res, i, tr, n);
     }
     if (NP == 1 && a.gain) gains(0, g0);  // (one row's latency: asked for with its elements)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) sum_of(px[i], pr[i], v[i]);
+    for (int i = 0; i < NP; ++i)
+      if (any(i)) sum_of(px[i], pr[i], v[i]);
   }
   double ss = 0;
   auto square = [&](int i, const float *h) {
+    if constexpr (VEC) {
+      if (!inside(i, 0)) return;
+    }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
-      const double d = inside(i, j) ? (double)h[j] : 0.0;
+      const double d = VEC || inside(i, j) ? (double)h[j] : 0.0;
       ss = fma(d, d, ss);
     }
   };
 #pragma unroll
-  for (int i = 0; i < NP; ++i) square(i, v[i]);
+  for (int i = 0; i < NP; ++i)
+    if (any(i)) square(i, v[i]);
   const int pieces = (n + kPiece * TR - 1) / (kPiece * TR);
   for (int i = NP; i < pieces; ++i) {
     float h[kPiece];
@@ -146,12 +163,17 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_norm_quant(NormArgs a) 
     if constexpr (TR > 64) {
       if ((threadIdx.x & 63) == 0) psum[threadIdx.x / 64] = ss;
       __syncthreads();
-      ss = psum[0];
+      double p[TR / 64];
 #pragma unroll
-      for (int i = 1; i < TR / 64; ++i) ss += psum[i];
+      for (int i = 0; i < TR / 64; ++i) p[i] = psum[i];
+#pragma unroll
+      for (int d = TR / 128; d >= 1; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i) p[i] += p[i + d];
+      ss = p[0];
     }
   }
-  const double r = 1.0 / sqrt(ss / (double)n + (double)a.eps);
+  const double r = inverse_root(ss * a.inv_n + (double)a.eps);
 
   auto norm = [&](int i, const float *h, const float *g, float *y) {
 #pragma unroll
@@ -163,12 +185,16 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_norm_quant(NormArgs a) 
   // read it, after it has; pieces that are read again are written last)
   int amax = 0;
   auto largest = [&](int i, const float *y) {
+    if constexpr (VEC) {
+      if (!inside(i, 0)) return;
+    }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j)
-      if (inside(i, j)) amax = max(amax, __float_as_int(y[j]) & 0x7fffffff);
+      if (VEC || inside(i, j)) amax = max(amax, __float_as_int(y[j]) & 0x7fffffff);
   };
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
+    if (!any(i)) continue;
     if (ho) P::template store<TR>(ho, i, tr, n, v[i]);
     float g[kPiece];
     if (NP > 1 && a.gain) gains(i, g);
@@ -184,12 +210,15 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_norm_quant(NormArgs a) 
       norm(i, h, g, h);
       largest(i, h);
     }
-    if constexpr (TR < 64) {
-#pragma unroll
-      for (int d = TR / 2; d >= 1; d >>= 1) amax = max(amax, __shfl_xor(amax, d, 64));
-    } else {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) amax = max(amax, __shfl_xor(amax, d, 64));
+    // (lanes outside a step's rows read 0, which is no larger)
+    amax = max(amax, dpp_i32<0xB1>(amax));
+    amax = max(amax, dpp_i32<0x4E>(amax));
+    amax = max(amax, dpp_i32<0x141>(amax));
+    amax = max(amax, dpp_i32<0x140>(amax));
+    if constexpr (TR >= 64) {
+      amax = max(amax, dpp_i32<0x142, 0xA>(amax));
+      amax = max(amax, dpp_i32<0x143, 0xC>(amax));
+      amax = __builtin_amdgcn_readlane(amax, 63);
       if constexpr (TR > 64) {
         if ((threadIdx.x & 63) == 0) pmax[threadIdx.x / 64] = amax;
         __syncthreads();
@@ -218,7 +247,8 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void k_norm_quant(NormArgs a) 
   };
   if (qo) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) put(i, v[i]);
+    for (int i = 0; i < NP; ++i)
+      if (any(i)) put(i, v[i]);
   }
   for (int i = NP; i < pieces; ++i) {
     float h[kPiece], g[kPiece];

@@ -50,6 +50,7 @@ struct NormArgs {
   const float *gain;    // [n]
   float eps;
   int T, n;
+  double inv_n;         // 1 / n
   void *h, *y;          // [T][n], row strides ldh, ldy
   int64_t ldh, ldy;
   int8_t *q;            // [T][n]
