@@ -334,14 +334,16 @@ coli_status coli_moe_forward_noalloc(const coli_moe_layer *L, const float *x,
  * integers.  Together they form a routed layer in 8 bits: coli_moe_route_scored,
  * coli_moe_dispatch, coli_quant_act_token, coli_gemm_q8_grouped (gate and up),
  * coli_swiglu_quant_token, coli_gemm_q8_grouped (down), coli_moe_combine; and
- * coli_gemm_q8 is the dense layers' product.
+ * coli_gemm_q8 is the dense layers' product.  coli_rmsnorm_quant_token stands in
+ * front of either, and coli_gemm_q8_lora is the dense product with the
+ * adapters of many requests.
  *
  * Every call takes its element type (coli_dtype) for activations and results;
  * scales, weights of the sum and biases are fp32.  Row strides (ld) are in
  * elements and at least the row's length; elements of a row are consecutive.
  * Rows that start 16-byte aligned are read and written in 16-byte words,
- * others element by element.  The calls need no workspace, keep nothing and
- * may be captured into a graph.  Buffers must not overlap unless stated.
+ * others element by element.  The calls need no workspace (coli_gemm_q8_lora
+ * excepted), keep nothing and may be captured into a graph.  Buffers must not overlap unless stated.
  * ------------------------------------------------------------------------- */
 typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
 
@@ -400,6 +402,53 @@ coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T,
                          const uint8_t *w, const float *ws, int32_t N,
                          int32_t K, const float *bias, int32_t dtype, void *y,
                          int64_t ldy, void *stream);
+
+/* Low-rank adapters of one projection (host struct of device pointers), stacked
+ * in slots: adapter l adds scale_l * b_l . (a_l . x).  Elements are of the call's
+ * dtype; a and b 16-byte aligned.  rank a multiple of 8 from 8 to 128 (an adapter
+ * of a lower rank is padded with zeros); 1 <= n_adapters <= 1024. */
+typedef struct {
+  int32_t n_adapters; /* L */
+  int32_t rank;       /* R */
+  const void *a;      /* [L][R][K] */
+  const void *b;      /* [L][N][R] */
+  const float *scale; /* [L] fp32, or NULL: 1 */
+} coli_lora;
+
+/* Workspace bytes of coli_gemm_q8_lora for up to max_tokens tokens and adapters of
+ * this rank (0 for arguments outside its limits).  A caller-owned device
+ * buffer, 256-byte aligned, holding the tokens' products with their adapters'
+ * a between the call's two launches; it needs no initial contents and keeps
+ * nothing between calls.  One workspace serves one call at a time: calls that may
+ * overlap (other streams, graphs replayed beside one another) need one each. */
+size_t coli_lora_workspace_bytes(int32_t max_tokens, int32_t rank);
+
+/* coli_gemm_q8 with the adapters of many requests beside it:
+ *   y [T][N] = s_t * ws_n * sum_k q[t][k] * w[n][k] (+ bias_n)
+ *              + scale_l * sum_r b[l][n][r] * u[t][r],
+ *   u[t][r] = sum_k a[l][r][k] * x[t][k],   l = ids[t].
+ * A token whose id is outside [0, L) has no adapter: its row is
+ * coli_gemm_q8's, bit for bit.  x [T][K], row stride ldx, are the activations of
+ * which q and s are the codes, in dtype like a, b and y.  ids [T] int32; offs
+ * [L + 1] and perm [T] are coli_moe_dispatch's tables of ids as one slot a token
+ * (k = 1, E = L), which one call makes for all projections of a batch; a token
+ * that they list under another adapter, or not at all, gets an undefined row.
+ * u and the adapters' sum are fp32 sums of fp32 (or exact 16-bit) products; u
+ * is not rounded to a 16-bit type between the two.  They are added to the
+ * projection's fp32 result, which is then rounded once to dtype.  The order of
+ * the fp32 sums goes by the batch's sizes, so a row with an adapter may differ in the
+ * last bits of fp32 from batch to batch; the same call gives the same bits.  An
+ * adapter that holds a NaN or an infinity makes only its own tokens' results
+ * NaN or infinite.  The rest, and the limits, as for coli_gemm_q8.
+ * COLI_ERR_WORKSPACE for a missing, misaligned or short workspace. */
+coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T,
+                              const uint8_t *w, const float *ws, int32_t N,
+                              int32_t K, const float *bias,
+                              const coli_lora *lora, const void *x, int64_t ldx,
+                              const int32_t *ids, const int32_t *offs,
+                              const int32_t *perm, int32_t dtype, void *y,
+                              int64_t ldy, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 /* The experts' form: for every position i in [offs[e], offs[e + 1]) of every
  * expert e, with p = perm[i], y[p] = the product of row p / fan of q with

@@ -78,6 +78,11 @@ class ScoreCfg(ctypes.Structure):
                 ("norm_topk_prob", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float)]
 
 
+class LoraC(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("a", _P), ("b", _P),
+                ("scale", _P)]
+
+
 class CacheLayoutC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("ctl", "slot_of", "expert_of", "last_use", "pinned", "use_count", "copy_list",
@@ -154,6 +159,9 @@ def _load(path: str) -> ctypes.CDLL:
         "coli_rmsnorm_quant_token": ([i32, _P, i64, _P, i64, _P, ctypes.c_float, i32, i32, _P, i64,
                                       _P, i64, _P, _P, _P], ctypes.c_int),
         "coli_gemm_q8": ([_P, _P, i32, _P, _P, i32, i32, _P, i32, _P, i64, _P], ctypes.c_int),
+        "coli_lora_workspace_bytes": ([i32, i32], sz),
+        "coli_gemm_q8_lora": ([_P, _P, i32, _P, _P, i32, i32, _P, ctypes.POINTER(LoraC), _P, i64,
+                               _P, _P, _P, i32, _P, i64, _P, sz, _P], ctypes.c_int),
         "coli_gemm_q8_grouped": ([_P, _P, i32, _P, _P, i32, i32, i32, _P, _P, i32, i32, i32, _P,
                                   i64, _P], ctypes.c_int),
         "coli_moe_combine": ([i32, _P, i64, _P, _P, i32, i32, i32, _P, i64, _P, i64, _P],
@@ -433,6 +441,68 @@ def coli_gemm_q8(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Te
         _dense(q, torch.int8, T * K, dev, "q"), _dense(s, torch.float32, T, dev, "s"), T,
         _dense(w, torch.uint8, N * K, dev, "w"), _dense(ws, torch.float32, N, dev, "ws"), N, K,
         None if bias is None else _dense(bias, torch.float32, N, dev, "bias"), dt, yp, ld,
+        _raw_stream(stream, dev)))
+
+
+class Lora:
+    """One projection's low-rank adapters: a [L, R, K], b [L, N, R] (one float
+    type, that of the calls' activations), scale fp32 [L] or None, and the C
+    descriptor that points at them.  The object keeps the tensors alive."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None):
+        _float_type(a, "a")
+        L, R, K = a.shape
+        N = b.shape[1]
+        if b.shape != (L, N, R):
+            raise ValueError(f"b must be [{L}, N, {R}], got {list(b.shape)}")
+        dev = _device_of(a, "a")
+        self.a, self.b, self.scale = a, b, scale
+        self.dtype, self.device, self.rank = a.dtype, dev, R
+        self.shape = L, R, K, N
+        self.c = LoraC(L, R, _dense(a, a.dtype, L * R * K, dev, "a"),
+                       _dense(b, a.dtype, L * N * R, dev, "b"),
+                       None if scale is None else _dense(scale, torch.float32, L, dev, "scale"))
+        self.ref = ctypes.byref(self.c)
+
+
+def coli_lora_workspace_bytes(max_tokens: int, rank: int) -> int:
+    return lib().coli_lora_workspace_bytes(max_tokens, rank)
+
+
+def lora_workspace(max_tokens: int, rank: int, device="cuda") -> torch.Tensor:
+    """A workspace for coli_gemm_q8_lora calls of up to max_tokens tokens."""
+    n = coli_lora_workspace_bytes(max_tokens, rank)
+    if n == 0:
+        raise ValueError(f"no workspace for {max_tokens} tokens of rank {rank}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def coli_gemm_q8_lora(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+                      lora: Lora, x: torch.Tensor, ids: torch.Tensor, offs: torch.Tensor,
+                      perm: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor,
+                      bias: torch.Tensor | None = None, stream=None) -> None:
+    """coli_gemm_q8 plus each token's adapter: q int8 [T, K], s fp32 [T], w uint8
+    [N, K] int8 codes, ws fp32 [N], x [T, K] the activations of the codes (rows may
+    be strided), ids int32 [T] adapters (none outside [0, L)), offs int32 [L + 1] and
+    perm int32 [T] coli_moe_dispatch's tables of ids [T, 1], bias fp32 [N] or None ->
+    y [T, N] (rows may be strided); x, y and the adapters of one float type.
+    workspace as lora_workspace makes it, for one call at a time."""
+    dev = _device_of(q, "q")
+    T, K = q.shape
+    L, R, Ka, N = lora.shape
+    dt = _float_type(y, "y")
+    if Ka != K or lora.dtype is not y.dtype or lora.device != dev:
+        raise ValueError(f"the adapters must be of {K} columns, {y.dtype} and on the current device, "
+                         f"got {Ka}, {lora.dtype} and device {lora.device}")
+    xp, ldx = _rowed(x, T, K, y.dtype, dev, "x")
+    yp, ldy = _rowed(y, T, N, y.dtype, dev, "y")
+    _check("coli_gemm_q8_lora", lib().coli_gemm_q8_lora(
+        _dense(q, torch.int8, T * K, dev, "q"), _dense(s, torch.float32, T, dev, "s"), T,
+        _dense(w, torch.uint8, N * K, dev, "w"), _dense(ws, torch.float32, N, dev, "ws"), N, K,
+        None if bias is None else _dense(bias, torch.float32, N, dev, "bias"), lora.ref, xp, ldx,
+        _dense(ids, torch.int32, T, dev, "ids"), _dense(offs, torch.int32, L + 1, dev, "offs"),
+        _dense(perm, torch.int32, T, dev, "perm"), dt, yp, ldy,
+        _dense(workspace, torch.uint8, workspace.numel(), dev, "workspace"), workspace.numel(),
         _raw_stream(stream, dev)))
 
 

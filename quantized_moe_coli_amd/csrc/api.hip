@@ -60,6 +60,8 @@ bool rows_ok(int d, const void *p, int64_t ld, int64_t n) {
   return p && aligned(p, dtype_size(d)) && ld >= n && ld <= (int64_t)1 << 40;
 }
 
+bool lora_rank_ok(int r) { return r >= 8 && r <= 128 && r % 8 == 0; }
+
 bool qtype_ok(int q) { return q == COLI_Q8 || q == COLI_Q4 || q == COLI_Q2; }
 
 bool router_ok(const coli_router_cfg *c) {
@@ -476,6 +478,40 @@ coli_status coli_gemm_q8(const int8_t *q, const float *s, int32_t T, const uint8
     const coli_status st = check_device();
     if (st != COLI_OK) return st;
     return from_hip(coli::launch_gemm_q8(dtype, a, static_cast<hipStream_t>(stream)));
+  });
+}
+
+size_t coli_lora_workspace_bytes(int32_t max_tokens, int32_t rank) {
+  if (max_tokens < 0 || max_tokens > kMaxTokens || !lora_rank_ok(rank)) return 0;
+  return align_up(coli::gemm_q8_lora_workspace(std::max(max_tokens, 1), rank), 256);
+}
+
+coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T, const uint8_t *w, const float *ws,
+                              int32_t N, int32_t K, const float *bias, const coli_lora *lora, const void *x,
+                              int64_t ldx, const int32_t *ids, const int32_t *offs, const int32_t *perm,
+                              int32_t dtype, void *y, int64_t ldy, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  return guarded([&] {
+    if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || N < 1 || K <= 0 || K % 32 || K > kMaxQ8Cols || !lora ||
+        lora->n_adapters < 1 || lora->n_adapters > 1024 || !lora_rank_ok(lora->rank))
+      return COLI_ERR_INVALID_ARG;
+    if (T == 0) return COLI_OK;
+    if (!q || !s || !w || !ws || !rows_ok(dtype, y, ldy, N) || !rows_ok(dtype, x, ldx, K) || !lora->a ||
+        !lora->b || !ids || !offs || !perm)
+      return COLI_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(s, 4) || !aligned(ws, 4) || !aligned(bias, 4) ||
+        !aligned(lora->a, 16) || !aligned(lora->b, 16) || !aligned(lora->scale, 4) || !aligned(ids, 4) ||
+        !aligned(offs, 4) || !aligned(perm, 4))
+      return COLI_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < coli_lora_workspace_bytes(T, lora->rank))
+      return COLI_ERR_WORKSPACE;
+    coli::Q8LoraArgs a{{q, s, w, ws, bias, y, ldy, T, N, K, 1, nullptr, nullptr, 0, 1}, x, ldx, lora->a, lora->b,
+                       lora->scale, ids, offs, perm, static_cast<float *>(workspace), lora->n_adapters,
+                       lora->rank, 1};
+    if (!coli::gemm_q8_fits(a)) return COLI_ERR_UNSUPPORTED;
+    const coli_status st = check_device();
+    if (st != COLI_OK) return st;
+    return from_hip(coli::launch_gemm_q8_lora(dtype, a, static_cast<hipStream_t>(stream)));
   });
 }
 

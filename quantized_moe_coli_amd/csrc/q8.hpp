@@ -1,5 +1,5 @@
 // q8.hpp -- shared by the kernels of the 8-bit products with one scale per
-// token and one per output channel (q8_quant.hip, norm_quant.hip, q8_gemm.hip)
+// token and one per output channel (q8_quant.hip, norm_quant.hip, q8_kernels.hpp)
 // and by the scored router (route_scored.hip): element types, and the launchers that
 // the C-ABI layer (api.hip) calls after checking every argument.
 #pragma once
@@ -82,6 +82,22 @@ struct Q8Args {
 // Whether the call's grid stays within a launch's limits.
 bool gemm_q8_fits(const Q8Args &a);
 hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st);
+
+// The dense product with low-rank adapters: L adapters a [L][R][K], b [L][N][R] of
+// y's type; ids [rows] a token's adapter (none outside [0, L)), tab_offs [L + 1]
+// and tab_perm [rows] the tokens by adapter; u [slices][rows][R] the tokens'
+// products with a, in parts of K.
+struct Q8LoraArgs : Q8Args {
+  const void *x;  // [rows][ldx]
+  int64_t ldx;
+  const void *a, *b;
+  const float *scale;  // [L] or null
+  const int32_t *ids, *tab_offs, *tab_perm;
+  float *u;
+  int L, R, slices;
+};
+size_t gemm_q8_lora_workspace(int T, int R);  // bytes of u
+hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, hipStream_t st);
 
 struct ScoreCfg {
   int E, k, n_group, topk_group, score, group_score, norm;

@@ -1,0 +1,189 @@
+// q8_lora.hip -- the dense 8-bit product with low-rank adapters of many
+// requests beside it:
+//   y[t][n] = s_t ws_n sum_k q[t][k] w[n][k] (+ bias[n]) + c_a sum_r u[t][r] b_a[n][r],
+//   u[t][r] = sum_k x[t][k] a_a[r][k],   a = ids[t].
+//
+// Two launches: u, by adapter over the batch's table of its tokens, into the
+// caller's workspace, and the product (q8_kernels.hpp), whose kernels add the
+// adapters' part to the sums in binary32 before their one rounding (lora.hpp).
+#include <algorithm>
+
+#include "q8_kernels.hpp"
+
+namespace coli {
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+// Eight operand elements of one row.
+template <int DT> struct Oper { typedef float type __attribute__((ext_vector_type(8))); };
+template <> struct Oper<COLI_BF16> { typedef v8bf type; };
+template <> struct Oper<COLI_F16> { typedef v8h type; };
+
+template <int DT, bool VEC>
+__device__ __forceinline__ typename Oper<DT>::type operand(const typename Elem<DT>::type *p) {
+  typedef typename Elem<DT>::type T;
+  typename Oper<DT>::type o;
+  if constexpr (VEC) {
+    constexpr int N = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 8 / N; ++k) {
+      const Pack<T, N> w = reinterpret_cast<const Pack<T, N> *>(p)[k];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[k * N + j] = w.v[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = p[j];
+  }
+  return o;
+}
+
+// 16 rows x 16 rows over k = 32, of which lane l has elements 8 (l / 16) ..
+// of row l % 16 of each.
+template <int DT>
+__device__ __forceinline__ v4f mul16(typename Oper<DT>::type w, typename Oper<DT>::type x, v4f c) {
+  if constexpr (DT == COLI_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
+  } else if constexpr (DT == COLI_F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// u of up to BM tokens of one adapter, over one of the slices of K.  The NW
+// waves share the slice's steps of 32 among them, and their sums are added
+// through LDS in order.  RT groups of 16 ranks (rows past R repeat its last).
+constexpr int kMaxSlices = 8;
+constexpr int kAhead = 4;  // steps a wave asks for together
+
+template <int DT, bool VEC, int BM, int NW, int RT>
+__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Oper<DT>::type O;
+  constexpr int TM = BM / 16;
+  __shared__ __align__(16) float part[NW][RT * 256];
+  __shared__ int rows[BM];
+  Q8Args tab{};
+  tab.E = g.L;
+  tab.P = g.rows;
+  tab.offs = g.tab_offs;
+  const Tile t = expert_tile<BM>(tab, g.slices);
+  if (t.n <= 0) return;
+  if (threadIdx.x < BM) {
+    const int p = g.tab_perm[t.r0 + min((int)threadIdx.x, t.n - 1)];
+    rows[threadIdx.x] = (int)threadIdx.x < t.n && (uint32_t)p < (uint32_t)g.rows ? p : -1;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int steps = g.K / 32;
+  const int first = (int)((int64_t)t.nb * steps / g.slices) + wave;
+  const int last = (int)((int64_t)(t.nb + 1) * steps / g.slices);
+
+  const T *xr[TM], *ar[RT];
+#pragma unroll
+  for (int j = 0; j < TM; ++j)
+    xr[j] = static_cast<const T *>(g.x) + max(rows[16 * j + li], 0) * g.ldx + 8 * lg;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    ar[i] = static_cast<const T *>(g.a) + ((int64_t)t.e * g.R + min(16 * i + li, g.R - 1)) * g.K + 8 * lg;
+  v4f acc[RT][TM];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  constexpr int AHEAD = (TM + RT) * (DT == COLI_F32 ? 2 : 1) > 8 ? 2 : kAhead;
+  for (int c = first; c < last; c += AHEAD * NW) {
+    O x[AHEAD][TM], w[AHEAD][RT];
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) {
+      const int64_t k = 32 * (int64_t)min(c + h * NW, last - 1);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) x[h][j] = operand<DT, VEC>(xr[j] + k);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) w[h][i] = operand<DT, true>(ar[i] + k);
+    }
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h)
+      if (c + h * NW < last) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[h][i], x[h][j], acc[i][j]);
+      }
+  }
+  // lane (li, lg) has token li's ranks 4 lg .. 4 lg + 3 of each 16
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    if (j > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f *>(&part[wave][i * 256 + 4 * lane]) = acc[i][j];
+    __syncthreads();
+    for (int o = threadIdx.x; o < RT * 64; o += 64 * NW) {
+      v4f sum = *reinterpret_cast<const v4f *>(&part[0][4 * o]);
+#pragma unroll
+      for (int w = 1; w < NW; ++w) sum += *reinterpret_cast<const v4f *>(&part[w][4 * o]);
+      const int row = rows[16 * j + (o & 15)], r = 16 * (o / 64) + 4 * ((o & 63) / 16);
+      if (row >= 0 && r < g.R)
+        *reinterpret_cast<v4f *>(g.u + ((int64_t)t.nb * g.rows + row) * g.R + r) = sum;
+    }
+  }
+}
+
+// Parts of K, so that a batch's tiles fill the chip even if one adapter has
+// all its tokens; the workspace's size bounds them too.
+int slices_of(int T, int bm) {
+  const int tiles = (T + bm - 1) / bm;
+  return std::max(1, std::min({kMaxSlices, 256 / tiles, 1 + 8192 / T}));
+}
+
+}  // namespace
+
+size_t gemm_q8_lora_workspace(int T, int R) {
+  return (size_t)std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192) * R * sizeof(float);
+}
+
+hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  const Variant v = dense_variant(a);
+  // tiles of 64 tokens where adapters have that many, on average over those
+  // that the caller holds
+  const bool many = a.rows / a.L >= 32;
+  const int bm = many ? 64 : 16;
+  a.slices = slices_of(a.rows, bm);
+  const int64_t tiles = a.rows / bm + std::min(a.rows, a.L);
+  const int64_t wgs = (tiles * a.slices + 7) / 8 * 8;
+  return by_dtype(dt, [&](auto dtc) {
+    constexpr int DT = decltype(dtc)::value;
+    typedef typename Elem<DT>::type T;
+    const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (uint64_t)a.ldx * sizeof(T) % 16 == 0;
+    auto go = [&](auto vecc, auto bmc, auto rtc) {
+      constexpr int BM = decltype(bmc)::value, NW = BM == 16 ? 8 : 4;
+      hipLaunchKernelGGL((k_lora_down<DT, decltype(vecc)::value, BM, NW, decltype(rtc)::value>), dim3(wgs),
+                         dim3(64 * NW), 0, st, a);
+    };
+    auto by_rank = [&](auto vecc, auto bmc) {
+      if (a.R <= 16) go(vecc, bmc, std::integral_constant<int, 1>());
+      else if (a.R <= 32) go(vecc, bmc, std::integral_constant<int, 2>());
+      else if (a.R <= 64) go(vecc, bmc, std::integral_constant<int, 4>());
+      else go(vecc, bmc, std::integral_constant<int, 8>());
+    };
+    auto by_tile = [&](auto vecc) {
+      if (many) by_rank(vecc, std::integral_constant<int, 64>());
+      else by_rank(vecc, std::integral_constant<int, 16>());
+    };
+    if (vec) by_tile(std::true_type());
+    else by_tile(std::false_type());
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    run_dense<DT>(a, v, st);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace coli
