@@ -506,12 +506,12 @@ coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T, const 
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < coli_lora_workspace_bytes(T, lora->rank))
       return COLI_ERR_WORKSPACE;
     coli::Q8LoraArgs a{{q, s, w, ws, bias, y, ldy, T, N, K, 1, nullptr, nullptr, 0, 1}, x, ldx, lora->a, lora->b,
-                       lora->scale, ids, offs, perm, static_cast<float *>(workspace), lora->n_adapters,
+                       lora->scale, ids, offs, perm, nullptr, nullptr, lora->n_adapters,
                        lora->rank, 1};
-    if (!coli::gemm_q8_fits(a)) return COLI_ERR_UNSUPPORTED;
+    if (!coli::gemm_q8_lora_fits(a)) return COLI_ERR_UNSUPPORTED;
     const coli_status st = check_device();
     if (st != COLI_OK) return st;
-    return from_hip(coli::launch_gemm_q8_lora(dtype, a, static_cast<hipStream_t>(stream)));
+    return from_hip(coli::launch_gemm_q8_lora(dtype, a, workspace, static_cast<hipStream_t>(stream)));
   });
 }
 

@@ -95,92 +95,184 @@ __device__ __forceinline__ void split8(const float *v, v8bf *o) {
   }
 }
 
-// The 32 tokens of group j (lane lr has token t, if `there`) and 32 TN channels
-// from nw on, by matrix instructions, one adapter of the group's tokens after
-// another.  A lane's results are one token's, so a token takes none of what
-// another's adapter gives, whatever it holds.  acc [TN][TMV] has the sums, and
-// gets the results as binary32 bits; chans [32 TN] their channels' scales, and
-// BN further their biases, in LDS.
+// The adapters' part of a tile of k_q8_tile, by matrix instructions, after its
+// sums.  The tile's tokens are in order of their adapters (the kernel takes them
+// by `order`), so they form runs; for each run the adapter's rows of b for the
+// tile's channels go through one of two buffers in LDS, the next run's on the
+// way while one is multiplied, and serve all the run's tokens.  u of all the
+// tile's tokens, times their adapters' scales, is put in LDS before, as bfloat16
+// pieces.  Ranks go by chunks of 128 bytes of b's rows.
 //
 // u stays in binary32: it enters as two bfloat16 pieces (2^-18 of it is lost
 // where the result has 8 or 11 bits) or three; adapters in fp16 as two, which
 // hold them whole, in fp32 as three.
-template <int DT, int TN, int TMV, int BN>
-__device__ __forceinline__ void lora_tile(const Q8LoraArgs &a, int t, bool there, float st, int nw,
-                                          const float *chans, int j, v16i (*acc)[TMV]) {
+//
+// A lane's results are one token's: where a group of 32 tokens has one adapter
+// its products go straight to the results, otherwise a token takes those of its
+// own adapter and none of another's, whatever they hold.
+template <int DT, int BM, int BN, int WM, int WN, int LDS>
+struct LoraTile {
   typedef typename Elem<DT>::type T;
-  constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = DT == COLI_F32 ? 3 : 2;
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  int id = a.ids[t];
-  if (!there || (uint32_t)id >= (uint32_t)a.L) id = -1;
-  const float f = id < 0 || !a.scale ? 1.f : a.scale[id];
-  // (read where they are used: held for the tile they would fill its registers)
-  auto at = [&](int i, int g, int off = 0) {
-    return reinterpret_cast<const Pack<float, 4> *>(chans + off + 32 * i + 8 * g + 4 * lh);
-  };
-  auto done = [&](const v16f *l, float f) {
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const Pack<float, 4> sn = *at(i, g), bn = *at(i, g, BN);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][4 * g + r] =
-              __float_as_int(finish(acc[i][j][4 * g + r], st, sn.v[r], fmaf(f, l[i][4 * g + r], bn.v[r])));
-      }
-  };
-  uint64_t todo = __ballot(id >= 0);
-  while (todo) {
-    const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    todo &= ~__ballot(id == e);
-    const T *b = static_cast<const T *>(a.b) + (int64_t)e * a.N * a.R;
-    v16f l[TN];
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) l[i][r] = 0.f;
-    for (int c = 0; c < a.R; c += 16) {
-      const int r = min(c + 8 * lh, a.R - 8);
-      const bool in = c + 8 * lh < a.R;
-      float v[8];
-      v8bf u[PU];
-      lora_u(a, t, r, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = in ? v[k] : 0.f;
-      split8<PU>(v, u);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        v8bf w[PB];
-        load8(b + (int64_t)min(nw + 32 * i + lr, a.N - 1) * a.R + r, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = in ? v[k] : 0.f;
-        split8<PB>(v, w);
-#pragma unroll
-        for (int p = 0; p < PB; ++p)
-#pragma unroll
-          for (int q = 0; q < PU; ++q)
-            if (p + q < (PB > PU ? PB : PU))
-              l[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[q], l[i], 0, 0, 0);
-      }
-    }
-    if (id == e) done(l, f);
+  static constexpr int NW = WM * WN, TN = BN / WN / 32;
+  static constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = DT == COLI_F32 ? 3 : 2;
+  static constexpr int KC = 128 / (int)sizeof(T);       // ranks of a chunk
+  static constexpr int UP = KC / 8;                     // 16-byte pieces of a row of u
+  static constexpr int UPLANE = BM * UP * 16, BBUF = BN * 128;
+  static constexpr int NL = BN * 8 / 64 / NW;           // loads of a wave for a whole chunk of b
+  static_assert(PU * UPLANE + 2 * BBUF <= LDS, "u and two buffers");
+
+  const Q8LoraArgs &a;
+  int n;            // tokens of the tile
+  unsigned char *lds;
+  const int *rows;  // [BM] tokens
+  const int *ids;   // [BM] their adapters, -1 none
+  const int *runs;  // first positions of the runs
+  int nruns;
+  const float *chans;  // [BN] the channels' scales, then their biases
+
+  __device__ __forceinline__ static int uplace(int row, int p) {
+    return (row * UP + (p ^ (UP == 8 ? row >> 1 & 7 : row >> 2 & 3))) * 16;
   }
-  if (id < 0) {
+  // place of piece p of row `row` of b, rows of pc pieces (lanes of 16 rows at one
+  // p meet all banks, but with 6 pieces half of them)
+  __device__ __forceinline__ static int bplace(int row, int p, int pc) {
+    return row * pc + (pc == 8 ? p ^ (row >> 1 & 7) : pc == 4 ? p ^ (row >> 2 & 3) : p);
+  }
+
+  // results of token `pos` of the tile: binary32 bits in place of the sums
+  __device__ __forceinline__ bool has(int pos) const { return pos < n && ids[pos] >= 0; }
+
+  template <int TMV>
+  __device__ __forceinline__ void add(v16i (*acc)[TMV], int n0) const {
+    const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+    for (int j = 0; j < TMV; ++j) {
+      const int pos = (j * WM + wm) * 32 + lr;
+      if (!has(pos)) continue;
+      const float st = a.s[max(rows[pos], 0)];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const Pack<float, 4> sn = *at(i, g), bn = *at(i, g, BN);
+      for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          // (rounded to y's type in the step itself, as without adapters)
-          const T y = (T)finish(acc[i][j][4 * g + r], st, sn.v[r], bn.v[r]);
-          acc[i][j][4 * g + r] = __float_as_int((float)y);
+        for (int g = 0; g < 4; ++g) {
+          const int at = (wn * TN + i) * 32 + 8 * g + 4 * lh;
+          const Pack<float, 4> sn = *reinterpret_cast<const Pack<float, 4> *>(chans + at);
+          const Pack<float, 4> bn = *reinterpret_cast<const Pack<float, 4> *>(chans + BN + at);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[i][j][4 * g + r] = __float_as_int(finish(acc[i][j][4 * g + r], st, sn.v[r], bn.v[r]));
+        }
+    }
+    const char *b0 = static_cast<const char *>(a.b) + (int64_t)n0 * a.R * sizeof(T);
+    for (int c = 0; c < a.R; c += KC) {
+      const int pc = min(8, (a.R - c) * (int)sizeof(T) / 16);
+      const uint32_t magic = 65536 / pc + 1;
+      uint32_t off[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int slot = ((i * NW + wave) * 64 + lane) & (BN * 8 - 1);
+        const int row = (int)(slot * magic >> 16);
+        off[i] = (uint32_t)(min(row, a.N - 1 - n0) * a.R + c) * (uint32_t)sizeof(T) +
+                 16 * (bplace(row, slot - row * pc, pc) - row * pc);
+      }
+      auto load_b = [&](int k) {
+        const int e = __builtin_amdgcn_readfirstlane(ids[runs[k]]);
+        if (e < 0) return;
+        const char *be = b0 + (int64_t)e * a.N * a.R * sizeof(T);
+        unsigned char *buf = lds + PU * UPLANE + (k & 1) * BBUF;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          if ((i * NW + wave) * 64 < BN * pc)
+            __builtin_amdgcn_global_load_lds(be + off[i], (__attribute__((address_space(3))) void *)(buf + (i * NW + wave) * 1024),
+                                             16, 0, 0);
+      };
+      lds_barrier();  // the sums' last operands, or the chunk before, have been read
+      load_b(0);
+      for (int o = threadIdx.x; o < n * UP; o += 64 * NW) {
+        const int row = o / UP, p = o % UP, r = c + 8 * p, e = ids[row];
+        if (r >= ((a.R + 15) & ~15) || e < 0) continue;
+        float v[8];
+        v8bf u[PU];
+        lora_u(a, max(rows[row], 0), min(r, a.R - 8), v);
+        const float f = r >= a.R ? 0.f : a.scale ? a.scale[e] : 1.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = r >= a.R ? 0.f : f * v[k];
+        split8<PU>(v, u);
+#pragma unroll
+        for (int q = 0; q < PU; ++q) *reinterpret_cast<v8bf *>(lds + q * UPLANE + uplace(row, p)) = u[q];
+      }
+      for (int k = 0; k < nruns; ++k) {
+        lds_barrier();  // this run's rows are there, and the run before has been multiplied
+        if (k + 1 < nruns) load_b(k + 1);
+        const int p0 = __builtin_amdgcn_readfirstlane(runs[k]);
+        const int p1 = k + 1 < nruns ? __builtin_amdgcn_readfirstlane(runs[k + 1]) : n;
+        if (__builtin_amdgcn_readfirstlane(ids[p0]) < 0) continue;
+        const unsigned char *buf = lds + PU * UPLANE + (k & 1) * BBUF;
+        const int steps = (min(KC, a.R - c) + 15) / 16;
+#pragma unroll
+        for (int j = 0; j < TMV; ++j) {
+          const int g0 = (j * WM + wm) * 32;
+          if (g0 >= p1 || g0 + 32 <= p0) continue;
+          const bool whole = p0 <= g0 && (p1 >= g0 + 32 || p1 == n);
+          const bool mine = g0 + lr >= p0 && g0 + lr < p1;
+#pragma unroll
+          for (int i = 0; i < TN; ++i) {
+            v16f l;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) l[r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
+            for (int s = 0; s < steps; ++s) {
+              v8bf u[PU], w[PB];
+#pragma unroll
+              for (int q = 0; q < PU; ++q)
+                u[q] = *reinterpret_cast<const v8bf *>(lds + q * UPLANE + uplace(g0 + lr, 2 * s + lh));
+              operand_b(buf, (wn * TN + i) * 32 + lr, 2 * s + lh, pc, c + 16 * s + 8 * lh < a.R, w);
+#pragma unroll
+              for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int q = 0; q < PU; ++q)
+                  if (p + q < (PB > PU ? PB : PU))
+                    l = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[q], l, 0, 0, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              acc[i][j][r] = whole  ? __float_as_int(l[r])
+                             : mine ? __float_as_int(__int_as_float(acc[i][j][r]) + l[r])
+                                    : acc[i][j][r];
+          }
         }
       }
+    }
   }
-}
+
+  // ranks 8 p .. 8 p + 7 of the chunk of row `row` of b, zero if not `in`
+  __device__ __forceinline__ static void operand_b(const unsigned char *buf, int row, int p, int pc, bool in,
+                                                   v8bf *w) {
+    if constexpr (PB == 1) {
+      w[0] = *reinterpret_cast<const v8bf *>(buf + 16 * bplace(row, p, pc));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[0][k] = in ? w[0][k] : (__bf16)0.f;
+    } else {
+      constexpr int N = 16 / (int)sizeof(T);
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 8 / N; ++h) {
+        const Pack<T, N> x = *reinterpret_cast<const Pack<T, N> *>(buf + 16 * bplace(row, 8 / N * p + h, pc));
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[h * N + k] = in ? (float)x.v[k] : 0.f;
+      }
+      split8<PB>(v, w);
+    }
+  }
+
+  // s_waitcnt vmcnt(0) lgkmcnt(0) and a barrier.
+  __device__ __forceinline__ static void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(7 << 4);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+};
 
 }  // namespace
 }  // namespace coli

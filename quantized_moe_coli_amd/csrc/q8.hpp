@@ -94,10 +94,12 @@ struct Q8LoraArgs : Q8Args {
   const float *scale;  // [L] or null
   const int32_t *ids, *tab_offs, *tab_perm;
   float *u;
+  int32_t *order;  // [rows] the tokens by adapter, those without one behind them
   int L, R, slices;
 };
-size_t gemm_q8_lora_workspace(int T, int R);  // bytes of u
-hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, hipStream_t st);
+bool gemm_q8_lora_fits(const Q8LoraArgs &a);
+size_t gemm_q8_lora_workspace(int T, int R);  // bytes of u and order
+hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_t st);
 
 struct ScoreCfg {
   int E, k, n_group, topk_group, score, group_score, norm;

@@ -381,10 +381,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(ARGS a, int nbm, 
 // hide one another's start and end (eight waves with 64 tokens take 1.17 times
 // as long).
 // ---------------------------------------------------------------------------
-template <int DT, int BM, int NW, int D, bool GROUPED, typename ARGS>
+template <int DT, int BM, int NW, int D, bool GROUPED>
 struct SweepKernel {
   typedef typename Elem<DT>::type T;
-  static constexpr bool LORA = std::is_same<ARGS, Q8LoraArgs>::value;
   static constexpr int BN = 32 * NW;
   static constexpr int SB = 128, PPR = 8;
   static constexpr int RINGB = (D + 1) * BM * SB;
@@ -393,7 +392,7 @@ struct SweepKernel {
   static constexpr int LDS = RINGB > AREAB ? RINGB : AREAB;
   __device__ __forceinline__ static int key(int r) { return (r >> 1) & 7; }
 
-  const ARGS &a;
+  const Q8Args &a;
   const Tile &t;
   unsigned char *ring;
   const int *rows;
@@ -573,10 +572,8 @@ struct SweepKernel {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         Pack<T, 4> v;
-        float b[4] = {bn[i][0], bn[i][1], bn[i][2], bn[i][3]};
-        if constexpr (LORA) lora_four<DT>(a, t.r0 + tt, n0 + 32 * wave + 16 * i + 4 * lg, b);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(acc[i][j][r], st, sn[i][r], b[r]);
+        for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(acc[i][j][r], st, sn[i][r], bn[i][r]);
         const int e = 32 * wave + 16 * i + 4 * lg;
         *reinterpret_cast<Pack<T, 4> *>(ring + li * ROWB + (((e / EPC) ^ (li & 7)) * 16) +
                                         (e % EPC) * (int)sizeof(T)) = v;
@@ -623,9 +620,9 @@ __device__ __forceinline__ void sweep_dispatch(K &k, int n) {
   }
 }
 
-template <int DT, int BM, int NW, int D, bool GROUPED, typename ARGS>
-__global__ __launch_bounds__(64 * NW) void k_q8_sweep(ARGS a, int nbm, int nbn) {
-  typedef SweepKernel<DT, BM, NW, D, GROUPED, ARGS> K;
+template <int DT, int BM, int NW, int D, bool GROUPED>
+__global__ __launch_bounds__(64 * NW) void k_q8_sweep(Q8Args a, int nbm, int nbn) {
+  typedef SweepKernel<DT, BM, NW, D, GROUPED> K;
   __shared__ __align__(16) unsigned char ring[K::LDS];
   __shared__ int rows[GROUPED ? BM : 1];
   Tile t;
@@ -692,6 +689,15 @@ struct TileKernel {
   unsigned char *ring;   // LDS bytes
   const int *rows;       // [BM] output rows of the tile's tokens (-1: none)
   const float *chans;    // [BN] the channels' scales (with adapters: and biases)
+  const int *ids;        // with adapters: LoraTile's
+  const int *runs;
+  int nruns;
+
+  // a row's row of q and s
+  __device__ __forceinline__ int src_row(int row) const {
+    if constexpr (LORA) return max(row, 0);
+    else return in_row<GROUPED>(a, row);
+  }
 
   template <int TMV>
   __device__ __forceinline__ void run() {
@@ -712,7 +718,7 @@ struct TileKernel {
 
     // this lane's source of each load: its row (tokens first, then weights)
     // and the piece of it that belongs at its place
-    const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.q) + (GROUPED ? 0 : (size_t)t.r0 * a.K);
+    const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.q) + (GROUPED || LORA ? 0 : (size_t)t.r0 * a.K);
     const uint8_t *wb = a.w + ((size_t)t.e * a.N + n0) * a.K;
     uint32_t off[NL], pl[NL];
     // first row of load i in the stage
@@ -728,7 +734,7 @@ struct TileKernel {
       int src;
       if (i < LX) {
         const int tt = min(r, t.n - 1);
-        src = GROUPED ? in_row<GROUPED>(a, rows[tt]) : tt;
+        src = GROUPED || LORA ? src_row(rows[tt]) : tt;
       } else {
         src = min(r - XROWS, a.N - 1 - n0);
       }
@@ -832,6 +838,8 @@ struct TileKernel {
     static_assert(64 % CH == 0 && CH <= 16 && NW * 32 * ROWB <= LDS, "whole rows a store, and the area");
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
+    if constexpr (LORA)
+      LoraTile<DT, BM, BN, WM, WN, LDS>{a, t.n, ring, rows, ids, runs, nruns, chans}.template add<TMV>(acc, n0);
     float sn[LORA ? 1 : TN][16], bn[LORA ? 1 : TN][16];
     if constexpr (!LORA) {
 #pragma unroll
@@ -851,10 +859,9 @@ struct TileKernel {
     for (int j = 0; j < TMV; ++j) {
       const int t0 = (j * WM + wm) * 32;
       if (t0 >= t.n) break;
-      const float st = a.s[in_row<GROUPED>(a, rows[min(t0 + lr, t.n - 1)])];
-      // with adapters the results as binary32 bits take the sums' place
-      if constexpr (LORA)
-        lora_tile<DT, TN, TMV, BN>(a, rows[min(t0 + lr, t.n - 1)], t0 + lr < t.n, st, nw, chans + (nw - n0), j, acc);
+      const float st = a.s[src_row(rows[min(t0 + lr, t.n - 1)])];
+      bool bare = false;  // the tokens without an adapter still have their sums
+      if constexpr (LORA) bare = ids[min(t0 + lr, t.n - 1)] < 0;
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -864,6 +871,19 @@ struct TileKernel {
           for (int r = 0; r < 4; ++r) {
             if constexpr (LORA) v.v[r] = (T)__int_as_float(acc[i][j][4 * g + r]);
             else v.v[r] = (T)finish(acc[i][j][4 * g + r], st, sn[i][4 * g + r], bn[i][4 * g + r]);
+          }
+          if constexpr (LORA) {
+            if (bare) {
+              const float *ch = chans + nw - n0 + 32 * i + 8 * g + 4 * lh;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                // (opaque: rounded in the step itself, as without adapters, and not
+                // after the two cases have met)
+                T o = (T)finish(acc[i][j][4 * g + r], st, ch[r], ch[BN + r]);
+                asm("" : "+v"(o));
+                v.v[r] = o;
+              }
+            }
           }
           const int e = 32 * i + 8 * g + 4 * lh;  // first element: chunk e / EPC, the key swaps chunks
           *reinterpret_cast<Pack<T, 4> *>(area + lr * ROWB + (((e / EPC) ^ (lr & 7)) * 16) +
@@ -919,7 +939,8 @@ __device__ __forceinline__ void tile_dispatch(K &k, int tm) {
 
 template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED, typename ARGS>
 __device__ __forceinline__ void tile_body(const ARGS &a, int nbm, int nbn, unsigned char *ring, int *rows,
-                                          float *chans) {
+                                          float *chans, int *ids) {
+  constexpr bool LORA = std::is_same<ARGS, Q8LoraArgs>::value;
   Tile t;
   if constexpr (GROUPED) {
     t = expert_tile<BM>(a, nbn);
@@ -935,14 +956,35 @@ __device__ __forceinline__ void tile_body(const ARGS &a, int nbm, int nbn, unsig
   }
   // (the channels' scales now, so that the end does not wait for them; the
   // tokens' too would fill the LDS to its last byte, which costs 13 %)
-  for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
+  if constexpr (LORA) {
+    // tokens by adapter, those without one last
+    for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) {
+      const int row = a.order[t.r0 + i];
+      rows[i] = (uint32_t)row < (uint32_t)a.rows ? row : -1;
+      const int e = rows[i] < 0 ? -1 : a.ids[row];
+      ids[i] = (uint32_t)e < (uint32_t)a.L ? e : -1;
+    }
+  } else {
+    for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
+  }
   for (int i = threadIdx.x; i < BN; i += 64 * WM * WN) {
     const int n = min(t.nb * BN + i, a.N - 1);
     chans[i] = a.ws[(size_t)t.e * a.N + n];
-    if constexpr (std::is_same<ARGS, Q8LoraArgs>::value) chans[BN + i] = a.bias ? a.bias[n] : 0.f;
+    if constexpr (LORA) chans[BN + i] = a.bias ? a.bias[n] : 0.f;
   }
   __syncthreads();
-  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS> k{a, t, ring, rows, chans};
+  int nruns = 0;
+  if constexpr (LORA) {  // each wave counts the runs of one adapter, and the first lists them
+    for (int p = 0; p < t.n; p += 64) {
+      const int i = p + (threadIdx.x & 63);
+      const bool first = i < t.n && (i == 0 || ids[i] != ids[i - 1]);
+      const uint64_t m = __ballot(first);
+      if (threadIdx.x < 64 && first)
+        ids[BM + nruns + __builtin_popcountll(m & (((uint64_t)1 << threadIdx.x) - 1))] = i;
+      nruns += __builtin_popcountll(m);
+    }
+  }
+  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS> k{a, t, ring, rows, chans, ids, ids + BM, nruns};
   tile_dispatch<BM / WM / 32>(k, (t.n + 32 * WM - 1) / (32 * WM));
 }
 
@@ -952,7 +994,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 :
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
   __shared__ __align__(16) float chans[std::is_same<ARGS, Q8LoraArgs>::value ? 2 * BN : BN];
-  tile_body<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS>(a, nbm, nbn, ring, rows, chans);
+  __shared__ int ids[std::is_same<ARGS, Q8LoraArgs>::value ? 2 * BM : 1];
+  tile_body<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS>(a, nbm, nbn, ring, rows, chans, ids);
 }
 
 // ---------------------------------------------------------------------------
@@ -1062,10 +1105,10 @@ void run_ring(const ARGS &a, int64_t wgs, hipStream_t st) {
                      dim3(64 * WM * WN * KS), 0, st, a, nbm, nbn);
 }
 
-template <int DT, bool GROUPED, int BM, int NW, int D, typename ARGS>
-void run_sweep(const ARGS &a, int64_t wgs, hipStream_t st) {
+template <int DT, bool GROUPED, int BM, int NW, int D>
+void run_sweep(const Q8Args &a, int64_t wgs, hipStream_t st) {
   const int nbn = (a.N + 32 * NW - 1) / (32 * NW), nbm = (a.rows + BM - 1) / BM;
-  hipLaunchKernelGGL((k_q8_sweep<DT, BM, NW, D, GROUPED, ARGS>), dim3(wgs), dim3(64 * NW), 0, st, a, nbm, nbn);
+  hipLaunchKernelGGL((k_q8_sweep<DT, BM, NW, D, GROUPED>), dim3(wgs), dim3(64 * NW), 0, st, a, nbm, nbn);
 }
 
 template <int DT, bool GROUPED, int BM, int BN, int WM, int WN, int LDS, typename ARGS>
@@ -1085,7 +1128,9 @@ void run_dense(const ARGS &a, Variant v, hipStream_t st) {
     case kRing32x64: run_ring<DT, false, 32, 64, 1, 1, 4, 3>(a, wgs, st); break;
     case kRing64x32: run_ring<DT, false, 64, 32, 2, 1, 4, 3>(a, wgs, st); break;
     case kRing64x64: run_ring<DT, false, 64, 64, 2, 2, 2, 2>(a, wgs, st); break;
-    case kSweep64: run_sweep<DT, false, 64, 4, 3>(a, wgs, st); break;
+    case kSweep64:
+      if constexpr (std::is_same<ARGS, Q8Args>::value) run_sweep<DT, false, 64, 4, 3>(a, wgs, st);
+      break;
     case kTile128: run_tile<DT, false, 128, 128, 2, 2, 64 << 10>(a, wgs, st); break;
     case kTile128Deep: run_tile<DT, false, 128, 128, 2, 2, 128 << 10>(a, wgs, st); break;
     default: run_tile<DT, false, 256, 256, 2, 4, 144 << 10>(a, wgs, st); break;

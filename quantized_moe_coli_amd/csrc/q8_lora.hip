@@ -55,6 +55,44 @@ __device__ __forceinline__ v4f mul16(typename Oper<DT>::type w, typename Oper<DT
   }
 }
 
+// The tokens in order of their adapters: the table's, and behind them, in order,
+// the tokens without one, which the table does not list.  Workgroup b writes the
+// table's part of positions kOrder b .. and the tokens without an adapter among
+// tokens kOrder b ..; those before them it counts itself.
+constexpr int kOrder = 1024;
+
+template <int NW>
+__device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *count) {
+  static_assert(NW <= 16 && kOrder % (64 * NW) == 0, "whole rounds");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
+  auto bare = [&](int t) { return t < g.rows && (uint32_t)g.ids[t] >= (uint32_t)g.L; };
+  int before = 0, mine = 0;  // (before: of this wave's share)
+  for (int t = threadIdx.x; t < t0; t += 64 * NW) before += bare(t);
+  uint64_t m[kOrder / 64 / NW];
+#pragma unroll
+  for (int i = 0; i < kOrder / 64 / NW; ++i) {
+    m[i] = __ballot(bare(t0 + (wave * (kOrder / 64 / NW) + i) * 64 + lane));
+    mine += __builtin_popcountll(m[i]);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) before += __shfl_xor(before, d, 64);
+  if (lane == 0) {
+    count[wave] = before;
+    count[16 + wave] = mine;
+  }
+  for (int i = t0 + threadIdx.x; i < min(t0 + kOrder, live); i += 64 * NW) g.order[i] = g.tab_perm[i];
+  __syncthreads();
+  int at = live;
+  for (int w = 0; w < NW; ++w) at += count[w] + (w < wave ? count[16 + w] : 0);
+#pragma unroll
+  for (int i = 0; i < kOrder / 64 / NW; ++i) {
+    const int to = at + __builtin_popcountll(m[i] & (((uint64_t)1 << lane) - 1));
+    if (m[i] >> lane & 1 && to < g.rows) g.order[to] = t0 + (wave * (kOrder / 64 / NW) + i) * 64 + lane;
+    at += __builtin_popcountll(m[i]);
+  }
+}
+
 // u of up to BM tokens of one adapter, over one of the slices of K.  The NW
 // waves share the slice's steps of 32 among them, and their sums are added
 // through LDS in order.  RT groups of 16 ranks (rows past R repeat its last).
@@ -62,12 +100,16 @@ constexpr int kMaxSlices = 8;
 constexpr int kAhead = 4;  // steps a wave asks for together
 
 template <int DT, bool VEC, int BM, int NW, int RT>
-__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g) {
+__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs) {
   typedef typename Elem<DT>::type T;
   typedef typename Oper<DT>::type O;
   constexpr int TM = BM / 16;
   __shared__ __align__(16) float part[NW][RT * 256];
-  __shared__ int rows[BM];
+  __shared__ int rows[BM < 32 ? 32 : BM];
+  if ((int)blockIdx.x >= wgs) {
+    order_tokens<NW>(g, blockIdx.x - wgs, rows);
+    return;
+  }
   Q8Args tab{};
   tab.E = g.L;
   tab.P = g.rows;
@@ -142,30 +184,51 @@ int slices_of(int T, int bm) {
   return std::max(1, std::min({kMaxSlices, 256 / tiles, 1 + 8192 / T}));
 }
 
+bool tiled(Variant v) { return v == kTile128 || v == kTile128Deep || v == kTile256; }
+
+// As without adapters, but for the sweep, which has no form with them: the
+// 128 x 128 tiles are within 13 % of the best of the forms there.
+Variant lora_variant(const Q8LoraArgs &a) {
+  const Variant v = dense_variant(a);
+  return v == kSweep64 ? kTile128 : v;
+}
+
+size_t order_bytes(int T) { return ((size_t)T * sizeof(int32_t) + 255) / 256 * 256; }
+
 }  // namespace
 
 size_t gemm_q8_lora_workspace(int T, int R) {
-  return (size_t)std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192) * R * sizeof(float);
+  return order_bytes(T) + (size_t)std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192) * R * sizeof(float);
 }
 
-hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, hipStream_t st) {
+bool gemm_q8_lora_fits(const Q8LoraArgs &a) {
+  const Variant v = lora_variant(a);
+  // (the tiles name rows of q by 32-bit byte offsets)
+  if (tiled(v) && (int64_t)a.rows * a.K >= (int64_t)1 << 32) return false;
+  return workgroups(a, v) * kShapes[v].threads < ((int64_t)1 << 31);
+}
+
+hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  const Variant v = dense_variant(a);
+  a.order = static_cast<int32_t *>(workspace);
+  a.u = reinterpret_cast<float *>(static_cast<char *>(workspace) + order_bytes(a.rows));
+  const Variant v = lora_variant(a);
   // tiles of 64 tokens where adapters have that many, on average over those
   // that the caller holds
   const bool many = a.rows / a.L >= 32;
   const int bm = many ? 64 : 16;
   a.slices = slices_of(a.rows, bm);
   const int64_t tiles = a.rows / bm + std::min(a.rows, a.L);
-  const int64_t wgs = (tiles * a.slices + 7) / 8 * 8;
+  const int wgs = (int)((tiles * a.slices + 7) / 8 * 8);
+  const int extra = tiled(v) ? (a.rows + kOrder - 1) / kOrder : 0;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     typedef typename Elem<DT>::type T;
     const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (uint64_t)a.ldx * sizeof(T) % 16 == 0;
     auto go = [&](auto vecc, auto bmc, auto rtc) {
       constexpr int BM = decltype(bmc)::value, NW = BM == 16 ? 8 : 4;
-      hipLaunchKernelGGL((k_lora_down<DT, decltype(vecc)::value, BM, NW, decltype(rtc)::value>), dim3(wgs),
-                         dim3(64 * NW), 0, st, a);
+      hipLaunchKernelGGL((k_lora_down<DT, decltype(vecc)::value, BM, NW, decltype(rtc)::value>), dim3(wgs + extra),
+                         dim3(64 * NW), 0, st, a, wgs);
     };
     auto by_rank = [&](auto vecc, auto bmc) {
       if (a.R <= 16) go(vecc, bmc, std::integral_constant<int, 1>());
