@@ -10,6 +10,10 @@
 namespace coli {
 namespace {
 
+// Whether a kernel's arguments are the product's with adapters.
+template <typename ARGS>
+constexpr bool kLora = std::is_same<ARGS, Q8LoraArgs>::value;
+
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -23,61 +27,105 @@ __device__ __forceinline__ float finish(int acc, float st, float sn, float b) {
   return __builtin_fmaf((float)acc * sn, st, b);
 }
 
-// u[t][r .. r + 7]
-__device__ __forceinline__ void lora_u(const Q8LoraArgs &a, int t, int r, float *u) {
-  const float *p = a.u + (int64_t)t * a.R + r;
-  *reinterpret_cast<Pack<float, 4> *>(u) = reinterpret_cast<const Pack<float, 4> *>(p)[0];
-  *reinterpret_cast<Pack<float, 4> *>(u + 4) = reinterpret_cast<const Pack<float, 4> *>(p)[1];
-  for (int s = 1; s < a.slices; ++s) {
-    p += (int64_t)a.rows * a.R;
-    const Pack<float, 4> lo = reinterpret_cast<const Pack<float, 4> *>(p)[0];
-    const Pack<float, 4> hi = reinterpret_cast<const Pack<float, 4> *>(p)[1];
+// u[t][r .. r + 3], of up to S parts of K, all asked for together
+template <int S>
+struct UParts {
+  Pack<float, 4> v[S];
+  __device__ __forceinline__ void load(const Q8LoraArgs &a, int t, int r) {
+    const float *p = a.u + (int64_t)t * a.R + r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[j] += lo.v[j];
-      u[4 + j] += hi.v[j];
-    }
+    for (int s = 0; s < S; ++s)
+      if (s < a.slices) v[s] = *reinterpret_cast<const Pack<float, 4> *>(p + (int64_t)s * a.rows * a.R);
   }
-}
-
-// Eight elements in 16-byte words.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *v) {
-  constexpr int N = 16 / (int)sizeof(T);
+  __device__ __forceinline__ Pack<float, 4> sum(const Q8LoraArgs &a) const {
+    Pack<float, 4> o = v[0];
 #pragma unroll
-  for (int k = 0; k < 8 / N; ++k) {
-    const Pack<T, N> w = reinterpret_cast<const Pack<T, N> *>(p)[k];
+    for (int s = 1; s < S; ++s)
+      if (s < a.slices) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[k * N + j] = (float)w.v[j];
+        for (int j = 0; j < 4; ++j) o.v[j] += v[s].v[j];
+      }
+    return o;
   }
-}
+};
 
-// Adds to d channels n .. n + 3 of token t, by vector instructions: with few tokens
-// nearly every one has an adapter of its own, and the work is reading them.
-template <int DT>
-__device__ __forceinline__ void lora_four(const Q8LoraArgs &a, int t, int n, float *d) {
+// Parts of K that a kernel of tiles of bm tokens takes u in.
+constexpr int lora_parts(int bm) { return bm == 16 ? 8 : 4; }
+
+// Adds the adapters' part to the biases of the 16 x 16 results that a wave of
+// k_q8_ring finishes, by vector instructions: with few tokens nearly every one has
+// an adapter of its own, and the work is reading it.  Lane (li, lg) has channels
+// 4 lg .. of token li.  What it needs is asked for while the last stages of the
+// sums are on their way: the first ranks of its rows of b, and its workgroup's
+// share of u, which goes through LDS for all the waves.  (As much is asked for
+// ahead as leaves the registers for two workgroups a CU.)
+template <int DT, int BM, int NT, int TPW>
+struct LoraRing {
   typedef typename Elem<DT>::type T;
-  const int id = a.ids[t];
-  if ((uint32_t)id >= (uint32_t)a.L) return;
-  float l[4] = {0.f, 0.f, 0.f, 0.f};
-  const T *b[4];
+  static constexpr int N = 16 / (int)sizeof(T);          // ranks of a 16-byte piece
+  static constexpr int FIRST = TPW > 1 && NT > 256 ? 0 : N / 4;  // eights of ranks asked for ahead
+  static constexpr int BYTES = BM * (128 + 4) * 4;       // u, rows of R + 4
+  int id[TPW];
+  Pack<T, N> w[TPW][FIRST ? FIRST : 1][4][8 / N];
+  UParts<lora_parts(BM)> part;
+  float scale[TPW];
+
+  __device__ __forceinline__ static void piece(Pack<T, N> *o, const T *p) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    b[r] = static_cast<const T *>(a.b) + ((int64_t)id * a.N + min(n + r, a.N - 1)) * a.R;
-  for (int p = 0; p < a.R; p += 8) {
-    float u[8], v[8];
-    lora_u(a, t, p, u);
+    for (int k = 0; k < 8 / N; ++k) o[k] = reinterpret_cast<const Pack<T, N> *>(p)[k];
+  }
+  // item o of u: token o / (R / 4), ranks 4 (o % (R / 4)) ..
+  __device__ __forceinline__ static int token(const Q8LoraArgs &a, int o) {
+    return (int)((uint32_t)o * (262144u / (uint32_t)a.R + 1) >> 16);  // (exact: o < 2^11, R / 4 <= 32)
+  }
+
+  // q: results (channels n ..) of token t
+  __device__ __forceinline__ void ask(const Q8LoraArgs &a, int q, int n) {
+    const int e = (uint32_t)id[q] < (uint32_t)a.L ? id[q] : 0;
+    scale[q] = a.scale ? a.scale[e] : 1.f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      load8(b[r] + p, v);
+    for (int p = 0; p < FIRST; ++p)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) l[r] = fmaf(u[j], v[j], l[r]);
+      for (int r = 0; r < 4; ++r) piece(w[q][p][r], row(a, e, n + r) + min(8 * p, a.R - 8));
+  }
+  __device__ __forceinline__ static const T *row(const Q8LoraArgs &a, int e, int n) {
+    return static_cast<const T *>(a.b) + ((int64_t)e * a.N + min(n, a.N - 1)) * a.R;
+  }
+  __device__ __forceinline__ void ask_u(const Q8LoraArgs &a, int t0, int n) {
+    const int o = threadIdx.x, t = token(a, o);
+    if (t < n) part.load(a, t0 + t, 4 * o - t * a.R);
+  }
+  __device__ __forceinline__ void put_u(const Q8LoraArgs &a, int t0, int n, float *us) {
+    for (int o = threadIdx.x; token(a, o) < n; o += NT) {
+      const int t = token(a, o), r = 4 * o - t * a.R;
+      if (o != (int)threadIdx.x) part.load(a, t0 + t, r);
+      *reinterpret_cast<Pack<float, 4> *>(us + t * (a.R + 4) + r) = part.sum(a);
     }
   }
-  const float f = a.scale ? a.scale[id] : 1.f;
+  __device__ __forceinline__ void add(const Q8LoraArgs &a, int q, int n, const float *u, float *d) const {
+    if ((uint32_t)id[q] >= (uint32_t)a.L) return;
+    float l[4] = {0.f, 0.f, 0.f, 0.f};
+    auto mul = [&](int p, int r, const Pack<T, N> *x) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) d[r] = fmaf(f, l[r], d[r]);
-}
+      for (int k = 0; k < 8; ++k) l[r] = fmaf(u[8 * p + k], (float)x[k / N].v[k % N], l[r]);
+    };
+#pragma unroll
+    for (int p = 0; p < FIRST; ++p)
+      if (8 * p < a.R) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mul(p, r, w[q][p][r]);
+      }
+    for (int p = FIRST; 8 * p < a.R; ++p) {
+      Pack<T, N> x[4][8 / N];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) piece(x[r], row(a, id[q], n + r) + 8 * p);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mul(p, r, x[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) d[r] = fmaf(scale[q], l[r], d[r]);
+  }
+};
 
 // v as a sum of P bfloat16 pieces, each the rounding of what is left: 8 bits a
 // piece and one more by the sign of the rest, so two hold 2^-18 of v, three all
@@ -119,6 +167,7 @@ struct LoraTile {
   static constexpr int UP = KC / 8;                     // 16-byte pieces of a row of u
   static constexpr int UPLANE = BM * UP * 16, BBUF = BN * 128;
   static constexpr int NL = BN * 8 / 64 / NW;           // loads of a wave for a whole chunk of b
+  static constexpr int UI = BM * UP / (64 * NW);        // eighths of a chunk's rows of u for a thread
   static_assert(PU * UPLANE + 2 * BBUF <= LDS, "u and two buffers");
 
   const Q8LoraArgs &a;
@@ -189,16 +238,42 @@ struct LoraTile {
       };
       lds_barrier();  // the sums' last operands, or the chunk before, have been read
       load_b(0);
-      for (int o = threadIdx.x; o < n * UP; o += 64 * NW) {
-        const int row = o / UP, p = o % UP, r = c + 8 * p, e = ids[row];
-        if (r >= ((a.R + 15) & ~15) || e < 0) continue;
-        float v[8];
-        v8bf u[PU];
-        lora_u(a, max(rows[row], 0), min(r, a.R - 8), v);
-        const float f = r >= a.R ? 0.f : a.scale ? a.scale[e] : 1.f;
+      // u: each thread has up to UI eighths of a chunk's row
+      float v[UI][8];
+      int at[UI];  // position and eighth, or -1
+      const float *up[UI];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = r >= a.R ? 0.f : f * v[k];
-        split8<PU>(v, u);
+      for (int i = 0; i < UI; ++i) {
+        const int o = i * 64 * NW + threadIdx.x, row = o / UP, r = c + 8 * (o % UP);
+        at[i] = row < n && r < ((a.R + 15) & ~15) && ids[min(row, n - 1)] >= 0 ? o : -1;
+        up[i] = a.u + (int64_t)max(rows[min(row, n - 1)], 0) * a.R + min(r, a.R - 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      }
+      for (int s = 0; s < a.slices; ++s) {
+        Pack<float, 4> x[UI][2];
+#pragma unroll
+        for (int i = 0; i < UI; ++i)
+          if (at[i] >= 0) {
+            x[i][0] = reinterpret_cast<const Pack<float, 4> *>(up[i])[0];
+            x[i][1] = reinterpret_cast<const Pack<float, 4> *>(up[i])[1];
+          }
+#pragma unroll
+        for (int i = 0; i < UI; ++i) {
+          up[i] += (int64_t)a.rows * a.R;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] += x[i][k / 4].v[k % 4];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < UI; ++i) {
+        if (at[i] < 0) continue;
+        const int row = at[i] / UP, p = at[i] % UP;
+        const float f = a.scale ? a.scale[ids[row]] : 1.f;
+        v8bf u[PU];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = c + 8 * p < a.R ? f * v[i][k] : 0.f;
+        split8<PU>(v[i], u);
 #pragma unroll
         for (int q = 0; q < PU; ++q) *reinterpret_cast<v8bf *>(lds + q * UPLANE + uplace(row, p)) = u[q];
       }

@@ -182,7 +182,7 @@ constexpr int kRingPieces = kRingBytes / 16;
 template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, bool GROUPED, typename ARGS>
 struct RingKernel {
   typedef typename Elem<DT>::type T;
-  static constexpr bool LORA = std::is_same<ARGS, Q8LoraArgs>::value;
+  static constexpr bool LORA = kLora<ARGS>;
   static constexpr int NW = WM * WN * KS;
   static constexpr int ROWS = BM + BN;
   static constexpr int NL = ROWS / 4 / NW;  // loads of a wave in a stage (4 rows each)
@@ -190,7 +190,8 @@ struct RingKernel {
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   static constexpr int STEPS = 4 / KS;      // steps of k = 64 of a wave in a stage
   static constexpr int PART = KS * BM * BN * 4;
-  static constexpr int LDS = STAGES * STAGE > PART ? STAGES * STAGE : PART;
+  static constexpr int AFTER = PART + (LORA ? BM * (128 + 4) * 4 : 0);  // what takes the ring's place at the end
+  static constexpr int LDS = STAGES * STAGE > AFTER ? STAGES * STAGE : AFTER;
   static_assert(ROWS % (4 * NW) == 0 && BM % 4 == 0 && 4 % KS == 0, "whole loads and steps");
 
   __device__ __forceinline__ static void run(const ARGS &a, const Tile &t, unsigned char *ring,
@@ -247,12 +248,10 @@ struct RingKernel {
         bn[q][r] = a.bias ? a.bias[nr] : 0.f;
       }
     }
-    if constexpr (LORA) {  // the adapters' part goes with the biases
+    typename std::conditional<LORA, LoraRing<DT, BM, 64 * NW, TPW>, int>::type lo;
+    if constexpr (LORA) {
 #pragma unroll
-      for (int q = 0; q < TPW; ++q) {
-        const int tl = min(q * NW + wave, TILES - 1);
-        lora_four<DT>(a, orow[q], n0 + (tl % (BN / 16)) * 16 + 4 * lg, bn[q]);
-      }
+      for (int q = 0; q < TPW; ++q) lo.id[q] = a.ids[orow[q]];
     }
     keep_order();
 
@@ -290,7 +289,8 @@ struct RingKernel {
       if (c < stages) issue(c);
       keep_order();
     }
-    for (int c = 0; c < stages; ++c) {
+    int c = 0;
+    auto stage = [&]() {
       // stage c has landed for every wave, and no wave reads stage c - 1 any more
       if (c + STAGES - 1 <= stages) stage_barrier<NL *(STAGES - 2)>();
       else stage_barrier<0>();
@@ -304,10 +304,21 @@ struct RingKernel {
         for (int s = 0; s < STEPS; ++s)
           if (4 * (kq * STEPS + s) < left) step(buf, kq * STEPS + s, left);
       }
+    };
+    if constexpr (LORA) {
+      for (; c + STAGES - 1 < stages; ++c) stage();
+      // (loads behind the stages': no wait for those counts too few)
+#pragma unroll
+      for (int q = 0; q < TPW; ++q) lo.ask(a, q, n0 + (min(q * NW + wave, TILES - 1) % (BN / 16)) * 16 + 4 * lg);
+      lo.ask_u(a, t.r0, t.n);
+      keep_order();
     }
+    for (; c < stages; ++c) stage();
 
     stage_barrier<0>();
     int *part = reinterpret_cast<int *>(ring);
+    float *us = reinterpret_cast<float *>(ring + PART);
+    if constexpr (LORA) lo.put_u(a, t.r0, t.n, us);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -328,6 +339,7 @@ struct RingKernel {
       for (int k = 1; k < KS; ++k)
         sum += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
       Pack<T, 4> v;
+      if constexpr (LORA) lo.add(a, q, n, us + tt * (a.R + 4), bn[q]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(sum[r], st[q], sn[q][r], bn[q][r]);
       T *d = y + (int64_t)orow[q] * a.ldy + n;
@@ -343,7 +355,8 @@ struct RingKernel {
 };
 
 template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, bool GROUPED, typename ARGS>
-__global__ __launch_bounds__(64 * WM * WN * KS) void k_q8_ring(ARGS a, int nbm, int nbn) {
+// (with adapters the larger ones would not leave the registers for two workgroups a CU)
+__global__ __launch_bounds__(64 * WM * WN * KS, kLora<ARGS> && WM * WN * KS == 8 ? 4 : 1) void k_q8_ring(ARGS a, int nbm, int nbn) {
   typedef RingKernel<DT, BM, BN, WM, WN, KS, STAGES, GROUPED, ARGS> K;
   __shared__ __align__(16) unsigned char ring[K::LDS];
   __shared__ int rows[GROUPED ? BM : 1];
@@ -671,7 +684,7 @@ __global__ __launch_bounds__(64 * NW) void k_q8_sweep(Q8Args a, int nbm, int nbn
 template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED, typename ARGS>
 struct TileKernel {
   typedef typename Elem<DT>::type T;
-  static constexpr bool LORA = std::is_same<ARGS, Q8LoraArgs>::value;
+  static constexpr bool LORA = kLora<ARGS>;
   static constexpr int SB = 128;
   static constexpr int NW = WM * WN;
   static constexpr int TN = BN / WN / 32;       // channel groups of a wave
@@ -940,7 +953,7 @@ __device__ __forceinline__ void tile_dispatch(K &k, int tm) {
 template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED, typename ARGS>
 __device__ __forceinline__ void tile_body(const ARGS &a, int nbm, int nbn, unsigned char *ring, int *rows,
                                           float *chans, int *ids) {
-  constexpr bool LORA = std::is_same<ARGS, Q8LoraArgs>::value;
+  constexpr bool LORA = kLora<ARGS>;
   Tile t;
   if constexpr (GROUPED) {
     t = expert_tile<BM>(a, nbn);
@@ -993,8 +1006,8 @@ template <int DT, int BM, int BN, int WM, int WN, int LDS, bool GROUPED, typenam
 __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 : 1) void k_q8_tile(ARGS a, int nbm, int nbn) {
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
-  __shared__ __align__(16) float chans[std::is_same<ARGS, Q8LoraArgs>::value ? 2 * BN : BN];
-  __shared__ int ids[std::is_same<ARGS, Q8LoraArgs>::value ? 2 * BM : 1];
+  __shared__ __align__(16) float chans[kLora<ARGS> ? 2 * BN : BN];
+  __shared__ int ids[kLora<ARGS> ? 2 * BM : 1];
   tile_body<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS>(a, nbm, nbn, ring, rows, chans, ids);
 }
 

@@ -94,43 +94,53 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *co
 }
 
 // u of up to BM tokens of one adapter, over one of the slices of K.  The NW
-// waves share the slice's steps of 32 among them, and their sums are added
-// through LDS in order.  RT groups of 16 ranks (rows past R repeat its last).
-constexpr int kMaxSlices = 8;
-constexpr int kAhead = 4;  // steps a wave asks for together
-
+// waves share the slice's lines (128 bytes of every row) among them, each with D
+// of its lines on the way, and their sums are added through LDS in order.  RT
+// groups of 16 ranks (rows past R repeat its last).  single: a tile is one token,
+// found by its id, with no table to look through.
 template <int DT, bool VEC, int BM, int NW, int RT>
-__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs) {
+__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs, bool single) {
   typedef typename Elem<DT>::type T;
   typedef typename Oper<DT>::type O;
   constexpr int TM = BM / 16;
+  constexpr int H = 4 / (int)sizeof(T);          // steps of k = 32 in a line
+  constexpr int D = TM + RT <= 3 ? 4 : TM + RT <= 5 ? 3 : 2;
   __shared__ __align__(16) float part[NW][RT * 256];
   __shared__ int rows[BM < 32 ? 32 : BM];
   if ((int)blockIdx.x >= wgs) {
     order_tokens<NW>(g, blockIdx.x - wgs, rows);
     return;
   }
-  Q8Args tab{};
-  tab.E = g.L;
-  tab.P = g.rows;
-  tab.offs = g.tab_offs;
-  const Tile t = expert_tile<BM>(tab, g.slices);
-  if (t.n <= 0) return;
-  if (threadIdx.x < BM) {
-    const int p = g.tab_perm[t.r0 + min((int)threadIdx.x, t.n - 1)];
-    rows[threadIdx.x] = (int)threadIdx.x < t.n && (uint32_t)p < (uint32_t)g.rows ? p : -1;
+  Tile t;
+  if (single) {
+    const int row = blockIdx.x / g.slices;
+    if (row >= g.rows) return;
+    t = Tile{g.ids[row], row, 1, (int)blockIdx.x % g.slices};
+    if ((uint32_t)t.e >= (uint32_t)g.L) return;
+    if (threadIdx.x < BM) rows[threadIdx.x] = threadIdx.x == 0 ? row : -1;
+  } else {
+    Q8Args tab{};
+    tab.E = g.L;
+    tab.P = g.rows;
+    tab.offs = g.tab_offs;
+    t = expert_tile<BM>(tab, g.slices);
+    if (t.n <= 0) return;
+    if (threadIdx.x < BM) {
+      const int p = g.tab_perm[t.r0 + min((int)threadIdx.x, t.n - 1)];
+      rows[threadIdx.x] = (int)threadIdx.x < t.n && (uint32_t)p < (uint32_t)g.rows ? p : -1;
+    }
   }
   __syncthreads();
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int steps = g.K / 32;
-  const int first = (int)((int64_t)t.nb * steps / g.slices) + wave;
-  const int last = (int)((int64_t)(t.nb + 1) * steps / g.slices);
+  const int lines = (g.K / 32 + H - 1) / H;
+  const int last = (int)((int64_t)(t.nb + 1) * lines / g.slices);
+  int c = (int)((int64_t)t.nb * lines / g.slices) + wave;
 
   const T *xr[TM], *ar[RT];
 #pragma unroll
   for (int j = 0; j < TM; ++j)
-    xr[j] = static_cast<const T *>(g.x) + max(rows[16 * j + li], 0) * g.ldx + 8 * lg;
+    xr[j] = static_cast<const T *>(g.x) + (single ? t.r0 : max(rows[16 * j + li], 0)) * g.ldx + 8 * lg;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
     ar[i] = static_cast<const T *>(g.a) + ((int64_t)t.e * g.R + min(16 * i + li, g.R - 1)) * g.K + 8 * lg;
@@ -139,25 +149,42 @@ __global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs) {
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  constexpr int AHEAD = (TM + RT) * (DT == COLI_F32 ? 2 : 1) > 8 ? 2 : kAhead;
-  for (int c = first; c < last; c += AHEAD * NW) {
-    O x[AHEAD][TM], w[AHEAD][RT];
+
+  O x[D][H][TM], w[D][H][RT];
+  // (lines past the slice's end ask for its last again; a half line for its first half)
+  auto load = [&](int d, int l) {
 #pragma unroll
-    for (int h = 0; h < AHEAD; ++h) {
-      const int64_t k = 32 * (int64_t)min(c + h * NW, last - 1);
+    for (int h = 0; h < H; ++h) {
+      const int k = min(32 * (H * min(l, last - 1) + h), g.K - 32);
 #pragma unroll
-      for (int j = 0; j < TM; ++j) x[h][j] = operand<DT, VEC>(xr[j] + k);
+      for (int j = 0; j < TM; ++j) x[d][h][j] = operand<DT, VEC>(xr[j] + k);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) w[h][i] = operand<DT, true>(ar[i] + k);
+      for (int i = 0; i < RT; ++i) w[d][h][i] = operand<DT, true>(ar[i] + k);
     }
+  };
+  auto mul = [&](int d, int l) {
 #pragma unroll
-    for (int h = 0; h < AHEAD; ++h)
-      if (c + h * NW < last) {
+    for (int h = 0; h < H; ++h)
+      if (32 * (H * l + h) < g.K) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[h][i], x[h][j], acc[i][j]);
+          for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[d][h][i], x[d][h][j], acc[i][j]);
       }
+  };
+  if (c < last) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, c + d * NW);
+    for (; c + D * NW < last; c += D * NW) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        mul(d, c + d * NW);
+        load(d, c + (D + d) * NW);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (c + d * NW < last) mul(d, c + d * NW);
   }
   // lane (li, lg) has token li's ranks 4 lg .. 4 lg + 3 of each 16
 #pragma unroll
@@ -177,11 +204,13 @@ __global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs) {
   }
 }
 
-// Parts of K, so that a batch's tiles fill the chip even if one adapter has
-// all its tokens; the workspace's size bounds them too.
-int slices_of(int T, int bm) {
-  const int tiles = (T + bm - 1) / bm;
-  return std::max(1, std::min({kMaxSlices, 256 / tiles, 1 + 8192 / T}));
+// Parts of K (a power of two), so that a batch's tiles fill the chip even if one
+// adapter has all its tokens; the workspace's size bounds them too.
+constexpr int kMaxSlices = 8;
+int slices_of(int T, int tiles, int most) {
+  int s = 1;
+  while (s < most && 2 * s * tiles <= 256 && 2 * s <= 1 + 8192 / T) s *= 2;
+  return s;
 }
 
 bool tiled(Variant v) { return v == kTile128 || v == kTile128Deep || v == kTile256; }
@@ -213,12 +242,12 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
   a.order = static_cast<int32_t *>(workspace);
   a.u = reinterpret_cast<float *>(static_cast<char *>(workspace) + order_bytes(a.rows));
   const Variant v = lora_variant(a);
-  // tiles of 64 tokens where adapters have that many, on average over those
-  // that the caller holds
-  const bool many = a.rows / a.L >= 32;
-  const int bm = many ? 64 : 16;
-  a.slices = slices_of(a.rows, bm);
-  const int64_t tiles = a.rows / bm + std::min(a.rows, a.L);
+  // a tile for each token where there are few; tiles of 32 tokens where adapters
+  // have that many, on average over those that the caller holds
+  const bool single = a.rows <= 64, many = a.rows / a.L >= 32;
+  const int bm = many ? 32 : 16;
+  a.slices = slices_of(a.rows, single ? a.rows : (a.rows + bm - 1) / bm, lora_parts(kShapes[v].bm));
+  const int64_t tiles = single ? a.rows : a.rows / bm + std::min(a.rows, a.L);
   const int wgs = (int)((tiles * a.slices + 7) / 8 * 8);
   const int extra = tiled(v) ? (a.rows + kOrder - 1) / kOrder : 0;
   return by_dtype(dt, [&](auto dtc) {
@@ -226,9 +255,9 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
     typedef typename Elem<DT>::type T;
     const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (uint64_t)a.ldx * sizeof(T) % 16 == 0;
     auto go = [&](auto vecc, auto bmc, auto rtc) {
-      constexpr int BM = decltype(bmc)::value, NW = BM == 16 ? 8 : 4;
+      constexpr int BM = decltype(bmc)::value, NW = 8;
       hipLaunchKernelGGL((k_lora_down<DT, decltype(vecc)::value, BM, NW, decltype(rtc)::value>), dim3(wgs + extra),
-                         dim3(64 * NW), 0, st, a, wgs);
+                         dim3(64 * NW), 0, st, a, wgs, single);
     };
     auto by_rank = [&](auto vecc, auto bmc) {
       if (a.R <= 16) go(vecc, bmc, std::integral_constant<int, 1>());
@@ -237,7 +266,7 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
       else go(vecc, bmc, std::integral_constant<int, 8>());
     };
     auto by_tile = [&](auto vecc) {
-      if (many) by_rank(vecc, std::integral_constant<int, 64>());
+      if (many) by_rank(vecc, std::integral_constant<int, 32>());
       else by_rank(vecc, std::integral_constant<int, 16>());
     };
     if (vec) by_tile(std::true_type());
