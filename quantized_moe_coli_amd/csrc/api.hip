@@ -507,7 +507,7 @@ coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T, const 
       return COLI_ERR_WORKSPACE;
     coli::Q8LoraArgs a{{q, s, w, ws, bias, y, ldy, T, N, K, 1, nullptr, nullptr, 0, 1}, x, ldx, lora->a, lora->b,
                        lora->scale, ids, offs, perm, nullptr, nullptr, lora->n_adapters,
-                       lora->rank, 1};
+                       lora->rank, 1, false};
     if (!coli::gemm_q8_lora_fits(a)) return COLI_ERR_UNSUPPORTED;
     const coli_status st = check_device();
     if (st != COLI_OK) return st;

@@ -1,6 +1,7 @@
 // lora.hpp -- the adapters' part of a product's results, as the kernels of
-// the 8-bit product add it: c_a sum_r u[t][r] b_a[n][r] for token t's adapter a,
-// with u [T][R] in binary32, in `slices` parts that are added in order.
+// the 8-bit product add it: c_a sum_r u[t][r] b_a[n][r] for token t's adapter a.
+// For the kernels of few tokens u [T][R] is in binary32, in `slices` parts that
+// are added in order.
 #pragma once
 
 #include "q8.hpp"
@@ -127,13 +128,16 @@ struct LoraRing {
   }
 };
 
+// Bfloat16 pieces of u for a type's results.
+constexpr int u_pieces(int dt) { return dt == COLI_F32 ? 3 : 2; }
+
 // v as a sum of P bfloat16 pieces, each the rounding of what is left: 8 bits a
 // piece and one more by the sign of the rest, so two hold 2^-18 of v, three all
 // of binary32.
-template <int P>
-__device__ __forceinline__ void split8(const float *v, v8bf *o) {
+template <int P, int M, typename V>
+__device__ __forceinline__ void split(const float *v, V *o) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < M; ++j) {
     float rest = v[j];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -142,210 +146,134 @@ __device__ __forceinline__ void split8(const float *v, v8bf *o) {
     }
   }
 }
+template <int P>
+__device__ __forceinline__ void split8(const float *v, v8bf *o) {
+  split<P, 8>(v, o);
+}
 
 // The adapters' part of a tile of k_q8_tile, by matrix instructions, after its
-// sums.  The tile's tokens are in order of their adapters (the kernel takes them
-// by `order`), so they form runs; for each run the adapter's rows of b for the
-// tile's channels go through one of two buffers in LDS, the next run's on the
-// way while one is multiplied, and serve all the run's tokens.  u of all the
-// tile's tokens, times their adapters' scales, is put in LDS before, as bfloat16
-// pieces.  Ranks go by chunks of 128 bytes of b's rows.
+// sums: for each group of 32 tokens one adapter of the group after another.  The
+// tile's tokens are in order of their adapters, so a group has few of them.  u
+// comes as bfloat16 pieces, times the adapters' scales, as k_lora_down leaves it for
+// these kernels, and goes with b's rows straight from memory to operand
+// registers, without LDS or a barrier.
 //
-// u stays in binary32: it enters as two bfloat16 pieces (2^-18 of it is lost
-// where the result has 8 or 11 bits) or three; adapters in fp16 as two, which
-// hold them whole, in fp32 as three.
+// u is a binary32 sum: two bfloat16 pieces lose 2^-18 of it where the result has 8
+// or 11 bits, three none.  Adapters in fp16 enter as two pieces, which hold them
+// whole, in fp32 as three.
 //
-// A lane's results are one token's: where a group of 32 tokens has one adapter
-// its products go straight to the results, otherwise a token takes those of its
-// own adapter and none of another's, whatever they hold.
-template <int DT, int BM, int BN, int WM, int WN, int LDS>
+// A lane's results are one token's: where a group has one adapter its products go
+// straight to the results, otherwise a token takes those of its own adapter and
+// none of another's, whatever they hold.
+template <int DT, int BM, int BN, int WM, int WN>
 struct LoraTile {
   typedef typename Elem<DT>::type T;
-  static constexpr int NW = WM * WN, TN = BN / WN / 32;
-  static constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = DT == COLI_F32 ? 3 : 2;
-  static constexpr int KC = 128 / (int)sizeof(T);       // ranks of a chunk
-  static constexpr int UP = KC / 8;                     // 16-byte pieces of a row of u
-  static constexpr int UPLANE = BM * UP * 16, BBUF = BN * 128;
-  static constexpr int NL = BN * 8 / 64 / NW;           // loads of a wave for a whole chunk of b
-  static constexpr int UI = BM * UP / (64 * NW);        // eighths of a chunk's rows of u for a thread
-  static_assert(PU * UPLANE + 2 * BBUF <= LDS, "u and two buffers");
+  static constexpr int TN = BN / WN / 32;
+  static constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = u_pieces(DT);
+  static constexpr int N = 16 / (int)sizeof(T), H = 8 / N;  // elements and words of an eighth of ranks
+  static constexpr int CS = H == 1 ? 2 : 1;                 // steps of 16 ranks asked for together
 
   const Q8LoraArgs &a;
   int n;            // tokens of the tile
-  unsigned char *lds;
   const int *rows;  // [BM] tokens
   const int *ids;   // [BM] their adapters, -1 none
-  const int *runs;  // first positions of the runs
-  int nruns;
   const float *chans;  // [BN] the channels' scales, then their biases
-
-  __device__ __forceinline__ static int uplace(int row, int p) {
-    return (row * UP + (p ^ (UP == 8 ? row >> 1 & 7 : row >> 2 & 3))) * 16;
-  }
-  // place of piece p of row `row` of b, rows of pc pieces (lanes of 16 rows at one
-  // p meet all banks, but with 6 pieces half of them)
-  __device__ __forceinline__ static int bplace(int row, int p, int pc) {
-    return row * pc + (pc == 8 ? p ^ (row >> 1 & 7) : pc == 4 ? p ^ (row >> 2 & 3) : p);
-  }
-
-  // results of token `pos` of the tile: binary32 bits in place of the sums
-  __device__ __forceinline__ bool has(int pos) const { return pos < n && ids[pos] >= 0; }
 
   template <int TMV>
   __device__ __forceinline__ void add(v16i (*acc)[TMV], int n0) const {
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
+    const int steps = (a.R + 15) / 16;
+    uint32_t boff[TN];  // of this lane's rows of an adapter's b, in elements
+#pragma unroll
+    for (int i = 0; i < TN; ++i) boff[i] = (uint32_t)(min(n0 + (wn * TN + i) * 32 + lr, a.N - 1) - n0) * (uint32_t)a.R;
 #pragma unroll
     for (int j = 0; j < TMV; ++j) {
-      const int pos = (j * WM + wm) * 32 + lr;
-      if (!has(pos)) continue;
-      const float st = a.s[max(rows[pos], 0)];
+      const int g0 = (j * WM + wm) * 32, pos = min(g0 + lr, n - 1);
+      if (g0 >= n) break;
+      const int id = g0 + lr < n ? ids[pos] : -1, row = max(rows[pos], 0);
+      uint64_t todo = __ballot(id >= 0);
+      if (id >= 0) {
+        const float st = a.s[row];
 #pragma unroll
-      for (int i = 0; i < TN; ++i)
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int at = (wn * TN + i) * 32 + 8 * g + 4 * lh;
-          const Pack<float, 4> sn = *reinterpret_cast<const Pack<float, 4> *>(chans + at);
-          const Pack<float, 4> bn = *reinterpret_cast<const Pack<float, 4> *>(chans + BN + at);
+          for (int g = 0; g < 4; ++g) {
+            const int at = (wn * TN + i) * 32 + 8 * g + 4 * lh;
+            const Pack<float, 4> sn = *reinterpret_cast<const Pack<float, 4> *>(chans + at);
+            const Pack<float, 4> bn = *reinterpret_cast<const Pack<float, 4> *>(chans + BN + at);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[i][j][4 * g + r] = __float_as_int(finish(acc[i][j][4 * g + r], st, sn.v[r], bn.v[r]));
-        }
-    }
-    const char *b0 = static_cast<const char *>(a.b) + (int64_t)n0 * a.R * sizeof(T);
-    for (int c = 0; c < a.R; c += KC) {
-      const int pc = min(8, (a.R - c) * (int)sizeof(T) / 16);
-      const uint32_t magic = 65536 / pc + 1;
-      uint32_t off[NL];
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int slot = ((i * NW + wave) * 64 + lane) & (BN * 8 - 1);
-        const int row = (int)(slot * magic >> 16);
-        off[i] = (uint32_t)(min(row, a.N - 1 - n0) * a.R + c) * (uint32_t)sizeof(T) +
-                 16 * (bplace(row, slot - row * pc, pc) - row * pc);
+            for (int r = 0; r < 4; ++r)
+              acc[i][j][4 * g + r] = __float_as_int(finish(acc[i][j][4 * g + r], st, sn.v[r], bn.v[r]));
+          }
       }
-      auto load_b = [&](int k) {
-        const int e = __builtin_amdgcn_readfirstlane(ids[runs[k]]);
-        if (e < 0) return;
-        const char *be = b0 + (int64_t)e * a.N * a.R * sizeof(T);
-        unsigned char *buf = lds + PU * UPLANE + (k & 1) * BBUF;
+      const __bf16 *u0 = reinterpret_cast<const __bf16 *>(a.u) + (int64_t)row * a.R;
+      while (todo) {
+        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t same = __ballot(id == e);
+        const bool whole = __ballot(g0 + lr < n && id != e) == 0;
+        todo &= ~same;
+        const T *b0 = static_cast<const T *>(a.b) + ((int64_t)e * a.N + n0) * a.R;
+        v16f l[TN];
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-          if ((i * NW + wave) * 64 < BN * pc)
-            __builtin_amdgcn_global_load_lds(be + off[i], (__attribute__((address_space(3))) void *)(buf + (i * NW + wave) * 1024),
-                                             16, 0, 0);
-      };
-      lds_barrier();  // the sums' last operands, or the chunk before, have been read
-      load_b(0);
-      // u: each thread has up to UI eighths of a chunk's row
-      float v[UI][8];
-      int at[UI];  // position and eighth, or -1
-      const float *up[UI];
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int i = 0; i < UI; ++i) {
-        const int o = i * 64 * NW + threadIdx.x, row = o / UP, r = c + 8 * (o % UP);
-        at[i] = row < n && r < ((a.R + 15) & ~15) && ids[min(row, n - 1)] >= 0 ? o : -1;
-        up[i] = a.u + (int64_t)max(rows[min(row, n - 1)], 0) * a.R + min(r, a.R - 8);
+          for (int r = 0; r < 16; ++r) l[i][r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
+        for (int s0 = 0; s0 < steps; s0 += CS) {
+          v8bf u[CS][PU];
+          Pack<T, N> b[CS][TN][H];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-      }
-      for (int s = 0; s < a.slices; ++s) {
-        Pack<float, 4> x[UI][2];
+          for (int s = 0; s < CS; ++s) {
+            const int r = min(16 * (s0 + s) + 8 * lh, a.R - 8);
 #pragma unroll
-        for (int i = 0; i < UI; ++i)
-          if (at[i] >= 0) {
-            x[i][0] = reinterpret_cast<const Pack<float, 4> *>(up[i])[0];
-            x[i][1] = reinterpret_cast<const Pack<float, 4> *>(up[i])[1];
+            for (int q = 0; q < PU; ++q)
+              u[s][q] = *reinterpret_cast<const v8bf *>(u0 + (int64_t)q * a.rows * a.R + r);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+              for (int h = 0; h < H; ++h) b[s][i][h] = reinterpret_cast<const Pack<T, N> *>(b0 + boff[i] + r)[h];
           }
 #pragma unroll
-        for (int i = 0; i < UI; ++i) {
-          up[i] += (int64_t)a.rows * a.R;
+          for (int s = 0; s < CS; ++s) {
+            if (s0 + s >= steps) continue;
+            if (16 * (s0 + s) + 8 * lh >= a.R) {  // ranks that are not there
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] += x[i][k / 4].v[k % 4];
-        }
-      }
+              for (int q = 0; q < PU; ++q) u[s][q] = v8bf{};
 #pragma unroll
-      for (int i = 0; i < UI; ++i) {
-        if (at[i] < 0) continue;
-        const int row = at[i] / UP, p = at[i] % UP;
-        const float f = a.scale ? a.scale[ids[row]] : 1.f;
-        v8bf u[PU];
+              for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = c + 8 * p < a.R ? f * v[i][k] : 0.f;
-        split8<PU>(v[i], u);
+                for (int h = 0; h < H; ++h) b[s][i][h] = Pack<T, N>{};
+            }
 #pragma unroll
-        for (int q = 0; q < PU; ++q) *reinterpret_cast<v8bf *>(lds + q * UPLANE + uplace(row, p)) = u[q];
-      }
-      for (int k = 0; k < nruns; ++k) {
-        lds_barrier();  // this run's rows are there, and the run before has been multiplied
-        if (k + 1 < nruns) load_b(k + 1);
-        const int p0 = __builtin_amdgcn_readfirstlane(runs[k]);
-        const int p1 = k + 1 < nruns ? __builtin_amdgcn_readfirstlane(runs[k + 1]) : n;
-        if (__builtin_amdgcn_readfirstlane(ids[p0]) < 0) continue;
-        const unsigned char *buf = lds + PU * UPLANE + (k & 1) * BBUF;
-        const int steps = (min(KC, a.R - c) + 15) / 16;
+            for (int i = 0; i < TN; ++i) {
+              v8bf w[PB];
+              if constexpr (PB == 1) {
+                __builtin_memcpy(&w[0], &b[s][i][0], 16);
+              } else {
+                float v[8];
 #pragma unroll
-        for (int j = 0; j < TMV; ++j) {
-          const int g0 = (j * WM + wm) * 32;
-          if (g0 >= p1 || g0 + 32 <= p0) continue;
-          const bool whole = p0 <= g0 && (p1 >= g0 + 32 || p1 == n);
-          const bool mine = g0 + lr >= p0 && g0 + lr < p1;
-#pragma unroll
-          for (int i = 0; i < TN; ++i) {
-            v16f l;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) l[r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
-            for (int s = 0; s < steps; ++s) {
-              v8bf u[PU], w[PB];
-#pragma unroll
-              for (int q = 0; q < PU; ++q)
-                u[q] = *reinterpret_cast<const v8bf *>(lds + q * UPLANE + uplace(g0 + lr, 2 * s + lh));
-              operand_b(buf, (wn * TN + i) * 32 + lr, 2 * s + lh, pc, c + 16 * s + 8 * lh < a.R, w);
+                for (int k = 0; k < 8; ++k) v[k] = (float)b[s][i][k / N].v[k % N];
+                split8<PB>(v, w);
+              }
 #pragma unroll
               for (int p = 0; p < PB; ++p)
 #pragma unroll
                 for (int q = 0; q < PU; ++q)
                   if (p + q < (PB > PU ? PB : PU))
-                    l = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[q], l, 0, 0, 0);
+                    l[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[s][q], l[i], 0, 0, 0);
             }
+          }
+        }
+        if (id == e || whole) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              acc[i][j][r] = whole  ? __float_as_int(l[r])
-                             : mine ? __float_as_int(__int_as_float(acc[i][j][r]) + l[r])
-                                    : acc[i][j][r];
-          }
+              acc[i][j][r] = __float_as_int(whole ? l[i][r] : __int_as_float(acc[i][j][r]) + l[i][r]);
         }
       }
     }
-  }
-
-  // ranks 8 p .. 8 p + 7 of the chunk of row `row` of b, zero if not `in`
-  __device__ __forceinline__ static void operand_b(const unsigned char *buf, int row, int p, int pc, bool in,
-                                                   v8bf *w) {
-    if constexpr (PB == 1) {
-      w[0] = *reinterpret_cast<const v8bf *>(buf + 16 * bplace(row, p, pc));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[0][k] = in ? w[0][k] : (__bf16)0.f;
-    } else {
-      constexpr int N = 16 / (int)sizeof(T);
-      float v[8];
-#pragma unroll
-      for (int h = 0; h < 8 / N; ++h) {
-        const Pack<T, N> x = *reinterpret_cast<const Pack<T, N> *>(buf + 16 * bplace(row, 8 / N * p + h, pc));
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[h * N + k] = in ? (float)x.v[k] : 0.f;
-      }
-      split8<PB>(v, w);
-    }
-  }
-
-  // s_waitcnt vmcnt(0) lgkmcnt(0) and a barrier.
-  __device__ __forceinline__ static void lds_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(7 << 4);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
   }
 };
 

@@ -94,8 +94,9 @@ struct Q8LoraArgs : Q8Args {
   const float *scale;  // [L] or null
   const int32_t *ids, *tab_offs, *tab_perm;
   float *u;
-  int32_t *order;  // [rows] the tokens by adapter, those without one behind them
+  int2 *order;  // [rows] tokens and their adapters, by adapter, those without one last
   int L, R, slices;
+  bool pieces;  // u [pieces][rows][R] as bfloat16 pieces, times the adapters' scales
 };
 bool gemm_q8_lora_fits(const Q8LoraArgs &a);
 size_t gemm_q8_lora_workspace(int T, int R);  // bytes of u and order

@@ -702,9 +702,7 @@ struct TileKernel {
   unsigned char *ring;   // LDS bytes
   const int *rows;       // [BM] output rows of the tile's tokens (-1: none)
   const float *chans;    // [BN] the channels' scales (with adapters: and biases)
-  const int *ids;        // with adapters: LoraTile's
-  const int *runs;
-  int nruns;
+  const int *ids;        // with adapters: [BM] the tokens', -1 none
 
   // a row's row of q and s
   __device__ __forceinline__ int src_row(int row) const {
@@ -852,7 +850,7 @@ struct TileKernel {
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
     if constexpr (LORA)
-      LoraTile<DT, BM, BN, WM, WN, LDS>{a, t.n, ring, rows, ids, runs, nruns, chans}.template add<TMV>(acc, n0);
+      LoraTile<DT, BM, BN, WM, WN>{a, t.n, rows, ids, chans}.template add<TMV>(acc, n0);
     float sn[LORA ? 1 : TN][16], bn[LORA ? 1 : TN][16];
     if constexpr (!LORA) {
 #pragma unroll
@@ -972,10 +970,10 @@ __device__ __forceinline__ void tile_body(const ARGS &a, int nbm, int nbn, unsig
   if constexpr (LORA) {
     // tokens by adapter, those without one last
     for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) {
-      const int row = a.order[t.r0 + i];
-      rows[i] = (uint32_t)row < (uint32_t)a.rows ? row : -1;
-      const int e = rows[i] < 0 ? -1 : a.ids[row];
-      ids[i] = (uint32_t)e < (uint32_t)a.L ? e : -1;
+      const int2 o = a.order[t.r0 + i];
+      const bool ok = (uint32_t)o.x < (uint32_t)a.rows;
+      rows[i] = ok ? o.x : -1;
+      ids[i] = ok && (uint32_t)o.y < (uint32_t)a.L ? o.y : -1;
     }
   } else {
     for (int i = threadIdx.x; i < t.n; i += 64 * WM * WN) rows[i] = out_row<GROUPED>(a, t.r0 + i);
@@ -986,18 +984,7 @@ __device__ __forceinline__ void tile_body(const ARGS &a, int nbm, int nbn, unsig
     if constexpr (LORA) chans[BN + i] = a.bias ? a.bias[n] : 0.f;
   }
   __syncthreads();
-  int nruns = 0;
-  if constexpr (LORA) {  // each wave counts the runs of one adapter, and the first lists them
-    for (int p = 0; p < t.n; p += 64) {
-      const int i = p + (threadIdx.x & 63);
-      const bool first = i < t.n && (i == 0 || ids[i] != ids[i - 1]);
-      const uint64_t m = __ballot(first);
-      if (threadIdx.x < 64 && first)
-        ids[BM + nruns + __builtin_popcountll(m & (((uint64_t)1 << threadIdx.x) - 1))] = i;
-      nruns += __builtin_popcountll(m);
-    }
-  }
-  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS> k{a, t, ring, rows, chans, ids, ids + BM, nruns};
+  TileKernel<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS> k{a, t, ring, rows, chans, ids};
   tile_dispatch<BM / WM / 32>(k, (t.n + 32 * WM - 1) / (32 * WM));
 }
 
@@ -1007,7 +994,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 || LDS <= 80 << 10 ? 2 :
   __shared__ __align__(16) unsigned char ring[LDS];
   __shared__ int rows[BM];
   __shared__ __align__(16) float chans[kLora<ARGS> ? 2 * BN : BN];
-  __shared__ int ids[kLora<ARGS> ? 2 * BM : 1];
+  __shared__ int ids[kLora<ARGS> ? BM : 1];
   tile_body<DT, BM, BN, WM, WN, LDS, GROUPED, ARGS>(a, nbm, nbn, ring, rows, chans, ids);
 }
 

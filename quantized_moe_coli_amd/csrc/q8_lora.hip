@@ -3,9 +3,9 @@
 //   y[t][n] = s_t ws_n sum_k q[t][k] w[n][k] (+ bias[n]) + c_a sum_r u[t][r] b_a[n][r],
 //   u[t][r] = sum_k x[t][k] a_a[r][k],   a = ids[t].
 //
-// Two launches: u, by adapter over the batch's table of its tokens, into the
-// caller's workspace, and the product (q8_kernels.hpp), whose kernels add the
-// adapters' part to the sums in binary32 before their one rounding (lora.hpp).
+// Two launches: u into the caller's workspace, and the product (q8_kernels.hpp),
+// whose kernels add the adapters' part to the sums in binary32 before their one
+// rounding (lora.hpp).  u is bound by reading x and the adapters' a once.
 #include <algorithm>
 
 #include "q8_kernels.hpp"
@@ -15,33 +15,15 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
-// Eight operand elements of one row.
-template <int DT> struct Oper { typedef float type __attribute__((ext_vector_type(8))); };
+// The 16 bytes of one row that a lane gives to a product, and 16 rows x 16 rows
+// over the 64 bytes of k that four lanes have of each row (lane l's are those of
+// row l % 16 at 16 (l / 16)).
+template <int DT> struct Oper { typedef v4f type; };
 template <> struct Oper<COLI_BF16> { typedef v8bf type; };
 template <> struct Oper<COLI_F16> { typedef v8h type; };
 
-template <int DT, bool VEC>
-__device__ __forceinline__ typename Oper<DT>::type operand(const typename Elem<DT>::type *p) {
-  typedef typename Elem<DT>::type T;
-  typename Oper<DT>::type o;
-  if constexpr (VEC) {
-    constexpr int N = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int k = 0; k < 8 / N; ++k) {
-      const Pack<T, N> w = reinterpret_cast<const Pack<T, N> *>(p)[k];
-#pragma unroll
-      for (int j = 0; j < N; ++j) o[k * N + j] = w.v[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = p[j];
-  }
-  return o;
-}
-
-// 16 rows x 16 rows over k = 32, of which lane l has elements 8 (l / 16) ..
-// of row l % 16 of each.
 template <int DT>
 __device__ __forceinline__ v4f mul16(typename Oper<DT>::type w, typename Oper<DT>::type x, v4f c) {
   if constexpr (DT == COLI_BF16) {
@@ -50,8 +32,24 @@ __device__ __forceinline__ v4f mul16(typename Oper<DT>::type w, typename Oper<DT
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, c, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w[j], x[j], c, 0, 0, 0);
     return c;
+  }
+}
+
+// u[row][r .. r + 3] of adapter e in slice sl
+template <int DT>
+__device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int e, int r, v4f u) {
+  if (g.pieces) {
+    const float f = g.scale ? g.scale[e] : 1.f;
+    const float v[4] = {f * u[0], f * u[1], f * u[2], f * u[3]};
+    v4bf o[u_pieces(DT)];
+    split<u_pieces(DT), 4>(v, o);
+    __bf16 *p = reinterpret_cast<__bf16 *>(g.u) + (int64_t)row * g.R + r;
+#pragma unroll
+    for (int q = 0; q < u_pieces(DT); ++q) *reinterpret_cast<v4bf *>(p + (int64_t)q * g.rows * g.R) = o[q];
+  } else {
+    *reinterpret_cast<v4f *>(g.u + ((int64_t)sl * g.rows + row) * g.R + r) = u;
   }
 }
 
@@ -64,15 +62,16 @@ constexpr int kOrder = 1024;
 template <int NW>
 __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *count) {
   static_assert(NW <= 16 && kOrder % (64 * NW) == 0, "whole rounds");
+  constexpr int M = kOrder / 64 / NW;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
   auto bare = [&](int t) { return t < g.rows && (uint32_t)g.ids[t] >= (uint32_t)g.L; };
   int before = 0, mine = 0;  // (before: of this wave's share)
   for (int t = threadIdx.x; t < t0; t += 64 * NW) before += bare(t);
-  uint64_t m[kOrder / 64 / NW];
+  uint64_t m[M];
 #pragma unroll
-  for (int i = 0; i < kOrder / 64 / NW; ++i) {
-    m[i] = __ballot(bare(t0 + (wave * (kOrder / 64 / NW) + i) * 64 + lane));
+  for (int i = 0; i < M; ++i) {
+    m[i] = __ballot(bare(t0 + (wave * M + i) * 64 + lane));
     mine += __builtin_popcountll(m[i]);
   }
 #pragma unroll
@@ -81,125 +80,193 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *co
     count[wave] = before;
     count[16 + wave] = mine;
   }
-  for (int i = t0 + threadIdx.x; i < min(t0 + kOrder, live); i += 64 * NW) g.order[i] = g.tab_perm[i];
+  for (int i = t0 + threadIdx.x; i < min(t0 + kOrder, live); i += 64 * NW) {
+    const int row = g.tab_perm[i];
+    g.order[i] = make_int2(row, (uint32_t)row < (uint32_t)g.rows ? g.ids[row] : -1);
+  }
   __syncthreads();
   int at = live;
   for (int w = 0; w < NW; ++w) at += count[w] + (w < wave ? count[16 + w] : 0);
 #pragma unroll
-  for (int i = 0; i < kOrder / 64 / NW; ++i) {
+  for (int i = 0; i < M; ++i) {
     const int to = at + __builtin_popcountll(m[i] & (((uint64_t)1 << lane) - 1));
-    if (m[i] >> lane & 1 && to < g.rows) g.order[to] = t0 + (wave * (kOrder / 64 / NW) + i) * 64 + lane;
+    if (m[i] >> lane & 1 && to < g.rows) g.order[to] = make_int2(t0 + (wave * M + i) * 64 + lane, -1);
     at += __builtin_popcountll(m[i]);
   }
 }
 
-// u of up to BM tokens of one adapter, over one of the slices of K.  The NW
-// waves share the slice's lines (128 bytes of every row) among them, each with D
-// of its lines on the way, and their sums are added through LDS in order.  RT
-// groups of 16 ranks (rows past R repeat its last).  single: a tile is one token,
-// found by its id, with no table to look through.
-template <int DT, bool VEC, int BM, int NW, int RT>
-__global__ __launch_bounds__(64 * NW) void k_lora_down(Q8LoraArgs g, int wgs, bool single) {
+constexpr int kDownWaves = 8;
+
+// Few tokens: a workgroup has one token and one slice of K.  Its waves share the
+// ranks; a wave reads 512 consecutive elements of a row of a at a time.
+template <int DT, bool VEC, int RW>
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down_one(Q8LoraArgs g, int wgs) {
+  typedef typename Elem<DT>::type T;
+  constexpr int N = 16 / (int)sizeof(T), H = 8 / N;
+  if ((int)blockIdx.x >= wgs) {
+    __shared__ int count[32];
+    order_tokens<kDownWaves>(g, blockIdx.x - wgs, count);
+    return;
+  }
+  const int row = blockIdx.x / g.slices, sl = blockIdx.x % g.slices;
+  const int e = row < g.rows ? g.ids[row] : -1;
+  if ((uint32_t)e >= (uint32_t)g.L) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave * RW >= g.R) return;
+  const int units = (g.K + 511) / 512;
+  const int last = (sl + 1) * units / g.slices;
+  const T *x = static_cast<const T *>(g.x) + row * g.ldx;
+  const T *a = static_cast<const T *>(g.a) + ((int64_t)e * g.R + wave * RW) * g.K;
+  float acc[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) acc[i] = 0.f;
+#pragma unroll 2
+  for (int u = sl * units / g.slices; u < last; ++u) {
+    const int k = 512 * u + 8 * lane, kk = min(k, g.K - 8);
+    float v[8];
+    Pack<T, N> w[RW][H];
+    if constexpr (VEC) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const Pack<T, N> p = reinterpret_cast<const Pack<T, N> *>(x + kk)[h];
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[h * N + j] = (float)p.v[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)x[kk + j];
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        w[i][h] = reinterpret_cast<const Pack<T, N> *>(a + (int64_t)min(i, g.R - 1 - wave * RW) * g.K + kk)[h];
+    if (k >= g.K) continue;
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i] = fmaf(v[j], (float)w[i][j / N].v[j % N], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < RW; ++i) acc[i] = group_sum<64>(acc[i]);
+  if (lane == 63) {
+#pragma unroll
+    for (int i = 0; i < RW; i += 4)
+      if (wave * RW + i < g.R)
+        put_u<DT>(g, sl, row, e, wave * RW + i, v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]});
+  }
+}
+
+// u of up to BM tokens of one adapter, over one of the slices of K, by matrix
+// instructions.  K goes by stages of 512 bytes of every row through a ring in LDS,
+// filled by direct loads of whole runs of two rows (16 rows' lines at one k, read
+// straight into operand registers, lie in one channel of the L2 where rows are a
+// multiple of 4 KB: 8192 x 6144 of rank 64 took 66-86 us so).  Each wave has 64 of
+// the 512 bytes of every row, and the waves' sums are added through LDS in order.
+// RT groups of 16 ranks (rows past R repeat its last).
+//
+// LDS: piece p (16 bytes) of row r's stage lies at place p ^ (r % 16).
+template <int DT, bool VEC, int BM, int RT, int STAGES>
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int wgs) {
   typedef typename Elem<DT>::type T;
   typedef typename Oper<DT>::type O;
-  constexpr int TM = BM / 16;
-  constexpr int H = 4 / (int)sizeof(T);          // steps of k = 32 in a line
-  constexpr int D = TM + RT <= 3 ? 4 : TM + RT <= 5 ? 3 : 2;
-  __shared__ __align__(16) float part[NW][RT * 256];
+  constexpr int NW = kDownWaves, ROWS = BM + 16 * RT, STAGE = ROWS * 512, PIECES = 32;
+  constexpr int TM = BM / 16, NL = ROWS / 16;  // loads of a wave in a stage, the tokens' TM first
+  constexpr int ASYNC = VEC ? NL : NL - TM;    // of them straight to LDS
+  static_assert(STAGES >= 2 && STAGES * STAGE >= NW * RT * 1024, "the sums take the ring's place");
+  __shared__ __align__(16) unsigned char ring[STAGES * STAGE];
   __shared__ int rows[BM < 32 ? 32 : BM];
   if ((int)blockIdx.x >= wgs) {
     order_tokens<NW>(g, blockIdx.x - wgs, rows);
     return;
   }
-  Tile t;
-  if (single) {
-    const int row = blockIdx.x / g.slices;
-    if (row >= g.rows) return;
-    t = Tile{g.ids[row], row, 1, (int)blockIdx.x % g.slices};
-    if ((uint32_t)t.e >= (uint32_t)g.L) return;
-    if (threadIdx.x < BM) rows[threadIdx.x] = threadIdx.x == 0 ? row : -1;
-  } else {
-    Q8Args tab{};
-    tab.E = g.L;
-    tab.P = g.rows;
-    tab.offs = g.tab_offs;
-    t = expert_tile<BM>(tab, g.slices);
-    if (t.n <= 0) return;
-    if (threadIdx.x < BM) {
-      const int p = g.tab_perm[t.r0 + min((int)threadIdx.x, t.n - 1)];
-      rows[threadIdx.x] = (int)threadIdx.x < t.n && (uint32_t)p < (uint32_t)g.rows ? p : -1;
-    }
+  Q8Args tab{};
+  tab.E = g.L;
+  tab.P = g.rows;
+  tab.offs = g.tab_offs;
+  const Tile t = expert_tile<BM>(tab, g.slices);
+  if (t.n <= 0) return;
+  if (threadIdx.x < BM) {
+    const int p = g.tab_perm[t.r0 + min((int)threadIdx.x, t.n - 1)];
+    rows[threadIdx.x] = (int)threadIdx.x < t.n && (uint32_t)p < (uint32_t)g.rows ? p : -1;
   }
   __syncthreads();
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lines = (g.K / 32 + H - 1) / H;
-  const int last = (int)((int64_t)(t.nb + 1) * lines / g.slices);
-  int c = (int)((int64_t)t.nb * lines / g.slices) + wave;
+  const int pieces = g.K / (16 / (int)sizeof(T)), stages = (pieces + PIECES - 1) / PIECES;
+  const int first = (int)((int64_t)t.nb * stages / g.slices), end = (int)((int64_t)(t.nb + 1) * stages / g.slices);
 
-  const T *xr[TM], *ar[RT];
+  const char *src[NL];
+  uint32_t pl[NL];
 #pragma unroll
-  for (int j = 0; j < TM; ++j)
-    xr[j] = static_cast<const T *>(g.x) + (single ? t.r0 : max(rows[16 * j + li], 0)) * g.ldx + 8 * lg;
+  for (int i = 0; i < NL; ++i) {
+    const int r = (i * NW + wave) * 2 + lane / 32;
+    pl[i] = (lane & 31) ^ (r & 15);
+    src[i] = i < TM ? static_cast<const char *>(g.x) + max(rows[r], 0) * g.ldx * (int64_t)sizeof(T)
+                    : static_cast<const char *>(g.a) +
+                          ((int64_t)t.e * g.R + min(r - BM, g.R - 1)) * g.K * (int64_t)sizeof(T);
+  }
+  auto issue = [&](int c) {
+    unsigned char *buf = ring + ((c - first) % STAGES) * STAGE;
+    const uint32_t last = min(PIECES, pieces - PIECES * c) - 1;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-    ar[i] = static_cast<const T *>(g.a) + ((int64_t)t.e * g.R + min(16 * i + li, g.R - 1)) * g.K + 8 * lg;
+    for (int i = 0; i < NL; ++i) {
+      const char *p = src[i] + (int64_t)c * 512 + 16 * min(pl[i], last);
+      unsigned char *to = buf + (i * NW + wave) * 1024;
+      if (VEC || i >= TM) {
+        __builtin_amdgcn_global_load_lds(p, (lds_void *)to, 16, 0, 0);
+      } else {  // rows that start at any element
+        Pack<T, 16 / (int)sizeof(T)> v;
+#pragma unroll
+        for (int k = 0; k < 16 / (int)sizeof(T); ++k) v.v[k] = reinterpret_cast<const T *>(p)[k];
+        *reinterpret_cast<Pack<T, 16 / (int)sizeof(T)> *>(to + 16 * lane) = v;
+      }
+    }
+  };
   v4f acc[RT][TM];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
-  O x[D][H][TM], w[D][H][RT];
-  // (lines past the slice's end ask for its last again; a half line for its first half)
-  auto load = [&](int d, int l) {
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int k = min(32 * (H * min(l, last - 1) + h), g.K - 32);
+  for (int c = 0; c < STAGES - 1; ++c) {
+    if (first + c < end) issue(first + c);
+    keep_order();
+  }
+  for (int c = first; c < end; ++c) {
+    // stage c has landed for every wave, and no wave reads stage c - 1 any more
+    if (c + STAGES - 1 <= end) stage_barrier<ASYNC *(STAGES - 2)>();
+    else stage_barrier<0>();
+    if (c + STAGES - 1 < end) issue(c + STAGES - 1);
+    const unsigned char *buf = ring + ((c - first) % STAGES) * STAGE + li * 512;
+    const int p = 4 * wave + lg;
+    if (PIECES * c + 4 * wave >= pieces) continue;  // (pieces are a multiple of 4)
+    O x[TM], w[RT];
 #pragma unroll
-      for (int j = 0; j < TM; ++j) x[d][h][j] = operand<DT, VEC>(xr[j] + k);
+    for (int j = 0; j < TM; ++j) x[j] = *reinterpret_cast<const O *>(buf + 16 * j * 512 + 16 * (p ^ li));
 #pragma unroll
-      for (int i = 0; i < RT; ++i) w[d][h][i] = operand<DT, true>(ar[i] + k);
-    }
-  };
-  auto mul = [&](int d, int l) {
+    for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const O *>(buf + (BM + 16 * i) * 512 + 16 * (p ^ li));
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (32 * (H * l + h) < g.K) {
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[d][h][i], x[d][h][j], acc[i][j]);
-      }
-  };
-  if (c < last) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(d, c + d * NW);
-    for (; c + D * NW < last; c += D * NW) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        mul(d, c + d * NW);
-        load(d, c + (D + d) * NW);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (c + d * NW < last) mul(d, c + d * NW);
+      for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[i], x[j], acc[i][j]);
   }
   // lane (li, lg) has token li's ranks 4 lg .. 4 lg + 3 of each 16
+  float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    if (j > 0) __syncthreads();
+    stage_barrier<0>();
 #pragma unroll
-    for (int i = 0; i < RT; ++i) *reinterpret_cast<v4f *>(&part[wave][i * 256 + 4 * lane]) = acc[i][j];
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<v4f *>(part + (wave * RT + i) * 256 + 4 * lane) = acc[i][j];
     __syncthreads();
-    for (int o = threadIdx.x; o < RT * 64; o += 64 * NW) {
-      v4f sum = *reinterpret_cast<const v4f *>(&part[0][4 * o]);
+    if (threadIdx.x < RT * 64) {
+      const int o = threadIdx.x;
+      v4f sum = *reinterpret_cast<const v4f *>(part + 4 * o);
 #pragma unroll
-      for (int w = 1; w < NW; ++w) sum += *reinterpret_cast<const v4f *>(&part[w][4 * o]);
+      for (int w = 1; w < NW; ++w) sum += *reinterpret_cast<const v4f *>(part + w * RT * 256 + 4 * o);
       const int row = rows[16 * j + (o & 15)], r = 16 * (o / 64) + 4 * ((o & 63) / 16);
-      if (row >= 0 && r < g.R)
-        *reinterpret_cast<v4f *>(g.u + ((int64_t)t.nb * g.rows + row) * g.R + r) = sum;
+      if (row >= 0 && r < g.R) put_u<DT>(g, t.nb, row, t.e, r, sum);
     }
   }
 }
@@ -222,12 +289,13 @@ Variant lora_variant(const Q8LoraArgs &a) {
   return v == kSweep64 ? kTile128 : v;
 }
 
-size_t order_bytes(int T) { return ((size_t)T * sizeof(int32_t) + 255) / 256 * 256; }
+size_t order_bytes(int T) { return ((size_t)T * sizeof(int2) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t gemm_q8_lora_workspace(int T, int R) {
-  return order_bytes(T) + (size_t)std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192) * R * sizeof(float);
+  const int64_t parts = 4 * std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192);
+  return order_bytes(T) + (size_t)std::max(parts, (int64_t)6 * T) * R;  // (three pieces of two bytes)
 }
 
 bool gemm_q8_lora_fits(const Q8LoraArgs &a) {
@@ -239,38 +307,46 @@ bool gemm_q8_lora_fits(const Q8LoraArgs &a) {
 
 hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  a.order = static_cast<int32_t *>(workspace);
+  a.order = static_cast<int2 *>(workspace);
   a.u = reinterpret_cast<float *>(static_cast<char *>(workspace) + order_bytes(a.rows));
   const Variant v = lora_variant(a);
-  // a tile for each token where there are few; tiles of 32 tokens where adapters
-  // have that many, on average over those that the caller holds
-  const bool single = a.rows <= 64, many = a.rows / a.L >= 32;
-  const int bm = many ? 32 : 16;
-  a.slices = slices_of(a.rows, single ? a.rows : (a.rows + bm - 1) / bm, lora_parts(kShapes[v].bm));
-  const int64_t tiles = single ? a.rows : a.rows / bm + std::min(a.rows, a.L);
+  a.pieces = tiled(v);
+  const bool one = a.rows <= 64;  // a workgroup for each token
+  const int bm = a.rows >= 4096 && a.R <= 64 ? 32 : 16;
+  const int least = one ? a.rows : (a.rows + bm - 1) / bm;
+  a.slices = a.pieces ? 1 : slices_of(a.rows, least, lora_parts(kShapes[v].bm));
+  const int64_t tiles = one ? a.rows : a.rows / bm + std::min(a.rows, a.L);
   const int wgs = (int)((tiles * a.slices + 7) / 8 * 8);
-  const int extra = tiled(v) ? (a.rows + kOrder - 1) / kOrder : 0;
+  const int extra = a.pieces ? (a.rows + kOrder - 1) / kOrder : 0;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     typedef typename Elem<DT>::type T;
     const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (uint64_t)a.ldx * sizeof(T) % 16 == 0;
-    auto go = [&](auto vecc, auto bmc, auto rtc) {
-      constexpr int BM = decltype(bmc)::value, NW = 8;
-      hipLaunchKernelGGL((k_lora_down<DT, decltype(vecc)::value, BM, NW, decltype(rtc)::value>), dim3(wgs + extra),
-                         dim3(64 * NW), 0, st, a, wgs, single);
+    const dim3 grid(wgs + extra), block(64 * kDownWaves);
+    auto few = [&](auto vecc) {
+      constexpr bool VEC = decltype(vecc)::value;
+      if (a.R <= 32) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 4>), grid, block, 0, st, a, wgs);
+      else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 8>), grid, block, 0, st, a, wgs);
+      else hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 16>), grid, block, 0, st, a, wgs);
     };
-    auto by_rank = [&](auto vecc, auto bmc) {
-      if (a.R <= 16) go(vecc, bmc, std::integral_constant<int, 1>());
-      else if (a.R <= 32) go(vecc, bmc, std::integral_constant<int, 2>());
-      else if (a.R <= 64) go(vecc, bmc, std::integral_constant<int, 4>());
-      else go(vecc, bmc, std::integral_constant<int, 8>());
+    // (stages: two workgroups a CU where two fit with a ring of three)
+    auto many = [&](auto vecc) {
+      constexpr bool VEC = decltype(vecc)::value;
+      if (bm == 16) {
+        if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 1, 4>), grid, block, 0, st, a, wgs);
+        else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 2, 3>), grid, block, 0, st, a, wgs);
+        else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 4, 3>), grid, block, 0, st, a, wgs);
+        else hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 8, 2>), grid, block, 0, st, a, wgs);
+      } else {
+        if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 1, 3>), grid, block, 0, st, a, wgs);
+        else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 2, 4>), grid, block, 0, st, a, wgs);
+        else hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 4, 3>), grid, block, 0, st, a, wgs);
+      }
     };
-    auto by_tile = [&](auto vecc) {
-      if (many) by_rank(vecc, std::integral_constant<int, 32>());
-      else by_rank(vecc, std::integral_constant<int, 16>());
-    };
-    if (vec) by_tile(std::true_type());
-    else by_tile(std::false_type());
+    if (one && vec) few(std::true_type());
+    else if (one) few(std::false_type());
+    else if (vec) many(std::true_type());
+    else many(std::false_type());
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     run_dense<DT>(a, v, st);
