@@ -128,7 +128,8 @@ struct LoraRing {
   }
 };
 
-// Bfloat16 pieces of u for a type's results.
+// Bfloat16 pieces of u for a type's results.  They lie [32 positions][16 ranks]
+// [piece][lane][8]: lane l has position l % 32 and ranks 8 (l / 32) .. of the 16.
 constexpr int u_pieces(int dt) { return dt == COLI_F32 ? 3 : 2; }
 
 // v as a sum of P bfloat16 pieces, each the rounding of what is left: 8 bits a
@@ -154,9 +155,10 @@ __device__ __forceinline__ void split8(const float *v, v8bf *o) {
 // The adapters' part of a tile of k_q8_tile, by matrix instructions, after its
 // sums: for each group of 32 tokens one adapter of the group after another.  The
 // tile's tokens are in order of their adapters, so a group has few of them.  u
-// comes as bfloat16 pieces, times the adapters' scales, as k_lora_down leaves it for
-// these kernels, and goes with b's rows straight from memory to operand
-// registers, without LDS or a barrier.
+// comes as bfloat16 pieces, times the adapters' scales, in the order of the operand
+// registers, as k_lora_down leaves it for these kernels, ranks from R to a multiple
+// of 16 zero; b's rows go straight from memory to registers too (past R a row's last
+// ranks again, of which the result has its part already), without LDS or a barrier.
 //
 // u is a binary32 sum: two bfloat16 pieces lose 2^-18 of it where the result has 8
 // or 11 bits, three none.  Adapters in fp16 enter as two pieces, which hold them
@@ -171,10 +173,10 @@ struct LoraTile {
   static constexpr int TN = BN / WN / 32;
   static constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = u_pieces(DT);
   static constexpr int N = 16 / (int)sizeof(T), H = 8 / N;  // elements and words of an eighth of ranks
-  static constexpr int CS = H == 1 ? 2 : 1;                 // steps of 16 ranks asked for together
+  static constexpr int CS = H == 1 ? 4 : 2;                 // steps of 16 ranks asked for together
 
   const Q8LoraArgs &a;
-  int n;            // tokens of the tile
+  int t0, n;        // first position and tokens of the tile
   const int *rows;  // [BM] tokens
   const int *ids;   // [BM] their adapters, -1 none
   const float *chans;  // [BN] the channels' scales, then their biases
@@ -188,14 +190,27 @@ struct LoraTile {
     uint32_t boff[TN];  // of this lane's rows of an adapter's b, in elements
 #pragma unroll
     for (int i = 0; i < TN; ++i) boff[i] = (uint32_t)(min(n0 + (wn * TN + i) * 32 + lr, a.N - 1) - n0) * (uint32_t)a.R;
+    int id[TMV];
+    float st[TMV];
 #pragma unroll
     for (int j = 0; j < TMV; ++j) {
-      const int g0 = (j * WM + wm) * 32, pos = min(g0 + lr, n - 1);
-      if (g0 >= n) break;
-      const int id = g0 + lr < n ? ids[pos] : -1, row = max(rows[pos], 0);
-      uint64_t todo = __ballot(id >= 0);
-      if (id >= 0) {
-        const float st = a.s[row];
+      const int pos = (j * WM + wm) * 32 + lr;
+      id[j] = pos < n ? ids[pos] : -1;
+      st[j] = a.s[max(rows[min(pos, n - 1)], 0)];
+    }
+    v8bf u[CS][PU];
+    auto load_u = [&](int j, int s0) {
+      const v8bf *p = reinterpret_cast<const v8bf *>(a.u) + ((int64_t)((t0 / 32 + j * WM + wm) * steps + s0) * PU) * 64;
+#pragma unroll
+      for (int s = 0; s < CS; ++s)
+        if (s0 + s < steps) {
+#pragma unroll
+          for (int q = 0; q < PU; ++q) u[s][q] = p[(s * PU + q) * 64 + lane];
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < TMV; ++j)
+      if (id[j] >= 0) {
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -205,72 +220,64 @@ struct LoraTile {
             const Pack<float, 4> bn = *reinterpret_cast<const Pack<float, 4> *>(chans + BN + at);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              acc[i][j][4 * g + r] = __float_as_int(finish(acc[i][j][4 * g + r], st, sn.v[r], bn.v[r]));
+              acc[i][j][4 * g + r] = __float_as_int(finish(acc[i][j][4 * g + r], st[j], sn.v[r], bn.v[r]));
           }
       }
-      const __bf16 *u0 = reinterpret_cast<const __bf16 *>(a.u) + (int64_t)row * a.R;
-      while (todo) {
-        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        const uint64_t same = __ballot(id == e);
-        const bool whole = __ballot(g0 + lr < n && id != e) == 0;
-        todo &= ~same;
-        const T *b0 = static_cast<const T *>(a.b) + ((int64_t)e * a.N + n0) * a.R;
-        v16f l[TN];
+    for (int s0 = 0; s0 < steps; s0 += CS) {
+      Pack<T, N> b[CS][TN][H];
+      int held = -1;  // the adapter whose rows are in b
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
+      for (int j = 0; j < TMV; ++j) {
+        const int g0 = (j * WM + wm) * 32;
+        uint64_t todo = __ballot(id[j] >= 0);
+        if (todo) load_u(j, s0);
+        while (todo) {
+          const int e = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(todo));
+          todo &= ~__ballot(id[j] == e);
+          const bool whole = __ballot(g0 + lr < n && id[j] != e) == 0;
+          if (e != held) {
+            const T *b0 = static_cast<const T *>(a.b) + ((int64_t)e * a.N + n0) * a.R;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) l[i][r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
-        for (int s0 = 0; s0 < steps; s0 += CS) {
-          v8bf u[CS][PU];
-          Pack<T, N> b[CS][TN][H];
+            for (int s = 0; s < CS; ++s)
+              if (s0 + s < steps) {
+                const int r = min(16 * (s0 + s) + 8 * lh, a.R - 8);
 #pragma unroll
-          for (int s = 0; s < CS; ++s) {
-            const int r = min(16 * (s0 + s) + 8 * lh, a.R - 8);
+                for (int i = 0; i < TN; ++i)
 #pragma unroll
-            for (int q = 0; q < PU; ++q)
-              u[s][q] = *reinterpret_cast<const v8bf *>(u0 + (int64_t)q * a.rows * a.R + r);
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-              for (int h = 0; h < H; ++h) b[s][i][h] = reinterpret_cast<const Pack<T, N> *>(b0 + boff[i] + r)[h];
-          }
-#pragma unroll
-          for (int s = 0; s < CS; ++s) {
-            if (s0 + s >= steps) continue;
-            if (16 * (s0 + s) + 8 * lh >= a.R) {  // ranks that are not there
-#pragma unroll
-              for (int q = 0; q < PU; ++q) u[s][q] = v8bf{};
-#pragma unroll
-              for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int h = 0; h < H; ++h) b[s][i][h] = Pack<T, N>{};
-            }
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-              v8bf w[PB];
-              if constexpr (PB == 1) {
-                __builtin_memcpy(&w[0], &b[s][i][0], 16);
-              } else {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = (float)b[s][i][k / N].v[k % N];
-                split8<PB>(v, w);
+                  for (int h = 0; h < H; ++h) b[s][i][h] = reinterpret_cast<const Pack<T, N> *>(b0 + boff[i] + r)[h];
               }
+            held = e;
+          }
 #pragma unroll
-              for (int p = 0; p < PB; ++p)
+          for (int i = 0; i < TN; ++i) {
+            v16f l;
 #pragma unroll
-                for (int q = 0; q < PU; ++q)
-                  if (p + q < (PB > PU ? PB : PU))
-                    l[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[s][q], l[i], 0, 0, 0);
+            for (int r = 0; r < 16; ++r) l[r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
+#pragma unroll
+            for (int s = 0; s < CS; ++s)
+              if (s0 + s < steps) {
+                v8bf w[PB];
+                if constexpr (PB == 1) {
+                  __builtin_memcpy(&w[0], &b[s][i][0], 16);
+                } else {
+                  float v[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[k] = (float)b[s][i][k / N].v[k % N];
+                  split8<PB>(v, w);
+                }
+#pragma unroll
+                for (int p = 0; p < PB; ++p)
+#pragma unroll
+                  for (int q = 0; q < PU; ++q)
+                    if (p + q < (PB > PU ? PB : PU))
+                      l = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[s][q], l, 0, 0, 0);
+              }
+            if (whole || id[j] == e) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                acc[i][j][r] = __float_as_int(whole ? l[r] : __int_as_float(acc[i][j][r]) + l[r]);
             }
           }
-        }
-        if (id == e || whole) {
-#pragma unroll
-          for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              acc[i][j][r] = __float_as_int(whole ? l[i][r] : __int_as_float(acc[i][j][r]) + l[i][r]);
         }
       }
     }

@@ -96,7 +96,7 @@ struct Q8LoraArgs : Q8Args {
   float *u;
   int2 *order;  // [rows] tokens and their adapters, by adapter, those without one last
   int L, R, slices;
-  bool pieces;  // u [pieces][rows][R] as bfloat16 pieces, times the adapters' scales
+  bool pieces;  // u as bfloat16 pieces, times the adapters' scales, by position in order (lora.hpp)
 };
 bool gemm_q8_lora_fits(const Q8LoraArgs &a);
 size_t gemm_q8_lora_workspace(int T, int R);  // bytes of u and order

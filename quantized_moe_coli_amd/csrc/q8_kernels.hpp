@@ -850,7 +850,7 @@ struct TileKernel {
     const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
     const int nw = n0 + wn * TN * 32;
     if constexpr (LORA)
-      LoraTile<DT, BM, BN, WM, WN>{a, t.n, rows, ids, chans}.template add<TMV>(acc, n0);
+      LoraTile<DT, BM, BN, WM, WN>{a, t.r0, t.n, rows, ids, chans}.template add<TMV>(acc, n0);
     float sn[LORA ? 1 : TN][16], bn[LORA ? 1 : TN][16];
     if constexpr (!LORA) {
 #pragma unroll

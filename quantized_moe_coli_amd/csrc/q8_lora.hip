@@ -37,18 +37,22 @@ __device__ __forceinline__ v4f mul16(typename Oper<DT>::type w, typename Oper<DT
   }
 }
 
-// u[row][r .. r + 3] of adapter e in slice sl
+// u[row][r .. r + 3] of adapter e in slice sl; pos is the token's position in order
 template <int DT>
-__device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int e, int r, v4f u) {
+__device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int pos, int e, int r, v4f u) {
   if (g.pieces) {
+    constexpr int PU = u_pieces(DT);
     const float f = g.scale ? g.scale[e] : 1.f;
-    const float v[4] = {f * u[0], f * u[1], f * u[2], f * u[3]};
-    v4bf o[u_pieces(DT)];
-    split<u_pieces(DT), 4>(v, o);
-    __bf16 *p = reinterpret_cast<__bf16 *>(g.u) + (int64_t)row * g.R + r;
+    float v[4];
 #pragma unroll
-    for (int q = 0; q < u_pieces(DT); ++q) *reinterpret_cast<v4bf *>(p + (int64_t)q * g.rows * g.R) = o[q];
-  } else {
+    for (int k = 0; k < 4; ++k) v[k] = r < g.R ? f * u[k] : 0.f;
+    v4bf o[PU];
+    split<PU, 4>(v, o);
+    char *p = reinterpret_cast<char *>(g.u) + (int64_t)(pos / 32 * ((g.R + 15) / 16) + r / 16) * PU * 1024 +
+              (r % 16 / 8 * 32 + pos % 32) * 16 + r % 8 * 2;
+#pragma unroll
+    for (int q = 0; q < PU; ++q) *reinterpret_cast<v4bf *>(p + q * 1024) = o[q];
+  } else if (r < g.R) {
     *reinterpret_cast<v4f *>(g.u + ((int64_t)sl * g.rows + row) * g.R + r) = u;
   }
 }
@@ -67,7 +71,15 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *co
   const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
   auto bare = [&](int t) { return t < g.rows && (uint32_t)g.ids[t] >= (uint32_t)g.L; };
   int before = 0, mine = 0;  // (before: of this wave's share)
-  for (int t = threadIdx.x; t < t0; t += 64 * NW) before += bare(t);
+  // (a run of eight loads at a time: t0 is a multiple of kOrder)
+  static_assert(kOrder % (8 * 64) == 0, "whole runs");
+  for (int t = threadIdx.x / 64 * 512 + lane; t < t0; t += 512 * NW) {
+    int e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = g.ids[t + 64 * i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) before += (uint32_t)e[i] >= (uint32_t)g.L;
+  }
   uint64_t m[M];
 #pragma unroll
   for (int i = 0; i < M; ++i) {
@@ -95,19 +107,12 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *co
   }
 }
 
-constexpr int kDownWaves = 8;
-
 // Few tokens: a workgroup has one token and one slice of K.  Its waves share the
 // ranks; a wave reads 512 consecutive elements of a row of a at a time.
 template <int DT, bool VEC, int RW>
-__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down_one(Q8LoraArgs g, int wgs) {
+__global__ __launch_bounds__(512) void k_lora_down_one(Q8LoraArgs g) {
   typedef typename Elem<DT>::type T;
   constexpr int N = 16 / (int)sizeof(T), H = 8 / N;
-  if ((int)blockIdx.x >= wgs) {
-    __shared__ int count[32];
-    order_tokens<kDownWaves>(g, blockIdx.x - wgs, count);
-    return;
-  }
   const int row = blockIdx.x / g.slices, sl = blockIdx.x % g.slices;
   const int e = row < g.rows ? g.ids[row] : -1;
   if ((uint32_t)e >= (uint32_t)g.L) return;
@@ -152,28 +157,35 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down_one(Q8LoraArgs g,
   if (lane == 63) {
 #pragma unroll
     for (int i = 0; i < RW; i += 4)
-      if (wave * RW + i < g.R)
-        put_u<DT>(g, sl, row, e, wave * RW + i, v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]});
+      put_u<DT>(g, sl, row, 0, e, wave * RW + i, v4f{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]});
   }
 }
 
 // u of up to BM tokens of one adapter, over one of the slices of K, by matrix
-// instructions.  K goes by stages of 512 bytes of every row through a ring in LDS,
-// filled by direct loads of whole runs of two rows (16 rows' lines at one k, read
-// straight into operand registers, lie in one channel of the L2 where rows are a
-// multiple of 4 KB: 8192 x 6144 of rank 64 took 66-86 us so).  Each wave has 64 of
-// the 512 bytes of every row, and the waves' sums are added through LDS in order.
-// RT groups of 16 ranks (rows past R repeat its last).
+// instructions.  K goes by stages of 256 bytes of every row through a ring in LDS,
+// filled by direct loads of whole runs of four rows (16 rows' lines at one k, read
+// straight into operand registers, took 1.2 to 1.5 times as long).  Each of the four
+// waves has 64 of the 256 bytes of every row, and the waves' sums are added through
+// LDS in order.  RT groups of 16 ranks (rows past R repeat its last).
 //
 // LDS: piece p (16 bytes) of row r's stage lies at place p ^ (r % 16).
-template <int DT, bool VEC, int BM, int RT, int STAGES>
-__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int wgs) {
+//
+// (Workgroups that each begin at another stage take 1.35 times as long: side by
+// side they read an adapter's a while it is near.)
+constexpr int down_stages(int bm, int rt) {
+  const int stage = (bm + 16 * rt) * 256, two = (78 << 10) / stage;  // two workgroups a CU
+  return two >= 3 ? (two < 8 ? two : 8) : (150 << 10) / stage;
+}
+
+template <int DT, bool VEC, int BM, int RT>
+__global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   typedef typename Elem<DT>::type T;
   typedef typename Oper<DT>::type O;
-  constexpr int NW = kDownWaves, ROWS = BM + 16 * RT, STAGE = ROWS * 512, PIECES = 32;
+  constexpr int NW = 4, ROWS = BM + 16 * RT, STAGE = ROWS * 256, PIECES = 16, STAGES = down_stages(BM, RT);
   constexpr int TM = BM / 16, NL = ROWS / 16;  // loads of a wave in a stage, the tokens' TM first
   constexpr int ASYNC = VEC ? NL : NL - TM;    // of them straight to LDS
-  static_assert(STAGES >= 2 && STAGES * STAGE >= NW * RT * 1024, "the sums take the ring's place");
+  static_assert(STAGES >= 3 && STAGES * STAGE >= NW * RT * 1024, "the sums take the ring's place");
+  static_assert(ASYNC * (STAGES - 1) < 64, "vmcnt range");
   __shared__ __align__(16) unsigned char ring[STAGES * STAGE];
   __shared__ int rows[BM < 32 ? 32 : BM];
   if ((int)blockIdx.x >= wgs) {
@@ -200,8 +212,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int
   uint32_t pl[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    const int r = (i * NW + wave) * 2 + lane / 32;
-    pl[i] = (lane & 31) ^ (r & 15);
+    const int r = (i * NW + wave) * 4 + lane / 16;
+    pl[i] = (lane & 15) ^ (r & 15);
     src[i] = i < TM ? static_cast<const char *>(g.x) + max(rows[r], 0) * g.ldx * (int64_t)sizeof(T)
                     : static_cast<const char *>(g.a) +
                           ((int64_t)t.e * g.R + min(r - BM, g.R - 1)) * g.K * (int64_t)sizeof(T);
@@ -211,7 +223,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int
     const uint32_t last = min(PIECES, pieces - PIECES * c) - 1;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const char *p = src[i] + (int64_t)c * 512 + 16 * min(pl[i], last);
+      const char *p = src[i] + (int64_t)c * 256 + 16 * min(pl[i], last);
       unsigned char *to = buf + (i * NW + wave) * 1024;
       if (VEC || i >= TM) {
         __builtin_amdgcn_global_load_lds(p, (lds_void *)to, 16, 0, 0);
@@ -238,14 +250,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int
     if (c + STAGES - 1 <= end) stage_barrier<ASYNC *(STAGES - 2)>();
     else stage_barrier<0>();
     if (c + STAGES - 1 < end) issue(c + STAGES - 1);
-    const unsigned char *buf = ring + ((c - first) % STAGES) * STAGE + li * 512;
-    const int p = 4 * wave + lg;
+    const unsigned char *buf = ring + ((c - first) % STAGES) * STAGE + li * 256 + 16 * ((4 * wave + lg) ^ li);
     if (PIECES * c + 4 * wave >= pieces) continue;  // (pieces are a multiple of 4)
     O x[TM], w[RT];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) x[j] = *reinterpret_cast<const O *>(buf + 16 * j * 512 + 16 * (p ^ li));
+    for (int j = 0; j < TM; ++j) x[j] = *reinterpret_cast<const O *>(buf + 16 * j * 256);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const O *>(buf + (BM + 16 * i) * 512 + 16 * (p ^ li));
+    for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const O *>(buf + (BM + 16 * i) * 256);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -260,13 +271,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(Q8LoraArgs g, int
     for (int i = 0; i < RT; ++i)
       *reinterpret_cast<v4f *>(part + (wave * RT + i) * 256 + 4 * lane) = acc[i][j];
     __syncthreads();
-    if (threadIdx.x < RT * 64) {
-      const int o = threadIdx.x;
+    for (int o = threadIdx.x; o < RT * 64; o += 64 * NW) {
       v4f sum = *reinterpret_cast<const v4f *>(part + 4 * o);
 #pragma unroll
       for (int w = 1; w < NW; ++w) sum += *reinterpret_cast<const v4f *>(part + w * RT * 256 + 4 * o);
-      const int row = rows[16 * j + (o & 15)], r = 16 * (o / 64) + 4 * ((o & 63) / 16);
-      if (row >= 0 && r < g.R) put_u<DT>(g, t.nb, row, t.e, r, sum);
+      const int i = 16 * j + (o & 15), r = 16 * (o / 64) + 4 * ((o & 63) / 16);
+      if (rows[i] >= 0 && r < ((g.R + 15) & ~15)) put_u<DT>(g, t.nb, rows[i], t.r0 + i, t.e, r, sum);
     }
   }
 }
@@ -294,8 +304,9 @@ size_t order_bytes(int T) { return ((size_t)T * sizeof(int2) + 255) / 256 * 256;
 }  // namespace
 
 size_t gemm_q8_lora_workspace(int T, int R) {
-  const int64_t parts = 4 * std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192);
-  return order_bytes(T) + (size_t)std::max(parts, (int64_t)6 * T) * R;  // (three pieces of two bytes)
+  const int64_t parts = 4 * std::min<int64_t>((int64_t)kMaxSlices * T, (int64_t)T + 8192) * R;
+  const int64_t pieces = 6 * (((int64_t)T + 31) / 32 * 32) * ((R + 15) / 16 * 16);  // (three of two bytes)
+  return order_bytes(T) + (size_t)std::max(parts, pieces);
 }
 
 bool gemm_q8_lora_fits(const Q8LoraArgs &a) {
@@ -311,42 +322,50 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
   a.u = reinterpret_cast<float *>(static_cast<char *>(workspace) + order_bytes(a.rows));
   const Variant v = lora_variant(a);
   a.pieces = tiled(v);
-  const bool one = a.rows <= 64;  // a workgroup for each token
-  const int bm = a.rows >= 4096 && a.R <= 64 ? 32 : 16;
-  const int least = one ? a.rows : (a.rows + bm - 1) / bm;
-  a.slices = a.pieces ? 1 : slices_of(a.rows, least, lora_parts(kShapes[v].bm));
-  const int64_t tiles = one ? a.rows : a.rows / bm + std::min(a.rows, a.L);
-  const int wgs = (int)((tiles * a.slices + 7) / 8 * 8);
+  const bool one = !a.pieces && a.rows <= 64;  // a workgroup for each token
+  const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : a.R <= 64 ? 4 : 8;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                   (uint64_t)a.ldx * (dt == COLI_F32 ? 4 : 2) % 16 == 0;
+  // Tokens of a tile: a tile costs its tokens' and its adapter's rows, and a CU
+  // works through its tiles one after another.  (8192 x 6144 of rank 64, 16 adapters:
+  // 272 tiles of 32 tokens 52-56 us, 187 of 48 MEASURE.)
+  int bm = 16;
+  if (!one && vec) {
+    int64_t least = INT64_MAX;
+    for (int m = 16; m <= 64; m += 16) {
+      const int64_t cost = (a.rows / m + std::min(a.rows, a.L) + 255) / 256 * (m + 16 * rt);
+      if (cost < least) least = cost, bm = m;
+    }
+  }
+  const int tiles = one ? a.rows : a.rows / bm + std::min(a.rows, a.L);  // at most
+  a.slices = a.pieces ? 1 : slices_of(a.rows, one ? a.rows : (a.rows + bm - 1) / bm, lora_parts(kShapes[v].bm));
+  const int wgs = (int)(((int64_t)tiles * a.slices + 7) / 8 * 8);
   const int extra = a.pieces ? (a.rows + kOrder - 1) / kOrder : 0;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
-    typedef typename Elem<DT>::type T;
-    const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (uint64_t)a.ldx * sizeof(T) % 16 == 0;
-    const dim3 grid(wgs + extra), block(64 * kDownWaves);
     auto few = [&](auto vecc) {
       constexpr bool VEC = decltype(vecc)::value;
-      if (a.R <= 32) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 4>), grid, block, 0, st, a, wgs);
-      else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 8>), grid, block, 0, st, a, wgs);
-      else hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 16>), grid, block, 0, st, a, wgs);
+      const dim3 grid(a.rows * a.slices), block(512);
+      if (a.R <= 32) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 4>), grid, block, 0, st, a);
+      else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 8>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((k_lora_down_one<DT, VEC, 16>), grid, block, 0, st, a);
     };
-    // (stages: two workgroups a CU where two fit with a ring of three)
-    auto many = [&](auto vecc) {
+    auto many = [&](auto vecc, auto bmc) {
       constexpr bool VEC = decltype(vecc)::value;
-      if (bm == 16) {
-        if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 1, 4>), grid, block, 0, st, a, wgs);
-        else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 2, 3>), grid, block, 0, st, a, wgs);
-        else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 4, 3>), grid, block, 0, st, a, wgs);
-        else hipLaunchKernelGGL((k_lora_down<DT, VEC, 16, 8, 2>), grid, block, 0, st, a, wgs);
-      } else {
-        if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 1, 3>), grid, block, 0, st, a, wgs);
-        else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 2, 4>), grid, block, 0, st, a, wgs);
-        else hipLaunchKernelGGL((k_lora_down<DT, VEC, 32, 4, 3>), grid, block, 0, st, a, wgs);
-      }
+      constexpr int BM = decltype(bmc)::value;
+      const dim3 grid(wgs + extra), block(256);
+      if (rt == 1) hipLaunchKernelGGL((k_lora_down<DT, VEC, BM, 1>), grid, block, 0, st, a, wgs);
+      else if (rt == 2) hipLaunchKernelGGL((k_lora_down<DT, VEC, BM, 2>), grid, block, 0, st, a, wgs);
+      else if (rt == 4) hipLaunchKernelGGL((k_lora_down<DT, VEC, BM, 4>), grid, block, 0, st, a, wgs);
+      else hipLaunchKernelGGL((k_lora_down<DT, VEC, BM, 8>), grid, block, 0, st, a, wgs);
     };
     if (one && vec) few(std::true_type());
     else if (one) few(std::false_type());
-    else if (vec) many(std::true_type());
-    else many(std::false_type());
+    else if (!vec) many(std::false_type(), std::integral_constant<int, 16>());
+    else if (bm == 16) many(std::true_type(), std::integral_constant<int, 16>());
+    else if (bm == 32) many(std::true_type(), std::integral_constant<int, 32>());
+    else if (bm == 48) many(std::true_type(), std::integral_constant<int, 48>());
+    else many(std::true_type(), std::integral_constant<int, 64>());
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     run_dense<DT>(a, v, st);
