@@ -17,7 +17,9 @@ constexpr bool kLora = std::is_same<ARGS, Q8LoraArgs>::value;
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 // y's element from the exact sum.  (The product of two small scales could be
 // subnormal where the result is not, so the sum comes first.  The last
@@ -53,81 +55,6 @@ struct UParts {
 // Parts of K that a kernel of tiles of bm tokens takes u in.
 constexpr int lora_parts(int bm) { return bm == 16 ? 8 : 4; }
 
-// Adds the adapters' part to the biases of the 16 x 16 results that a wave of
-// k_q8_ring finishes, by vector instructions: with few tokens nearly every one has
-// an adapter of its own, and the work is reading it.  Lane (li, lg) has channels
-// 4 lg .. of token li.  What it needs is asked for while the last stages of the
-// sums are on their way: the first ranks of its rows of b, and its workgroup's
-// share of u, which goes through LDS for all the waves.  (As much is asked for
-// ahead as leaves the registers for two workgroups a CU.)
-template <int DT, int BM, int NT, int TPW>
-struct LoraRing {
-  typedef typename Elem<DT>::type T;
-  static constexpr int N = 16 / (int)sizeof(T);          // ranks of a 16-byte piece
-  static constexpr int FIRST = TPW > 1 && NT > 256 ? 0 : N / 4;  // eights of ranks asked for ahead
-  static constexpr int BYTES = BM * (128 + 4) * 4;       // u, rows of R + 4
-  int id[TPW];
-  Pack<T, N> w[TPW][FIRST ? FIRST : 1][4][8 / N];
-  UParts<lora_parts(BM)> part;
-  float scale[TPW];
-
-  __device__ __forceinline__ static void piece(Pack<T, N> *o, const T *p) {
-#pragma unroll
-    for (int k = 0; k < 8 / N; ++k) o[k] = reinterpret_cast<const Pack<T, N> *>(p)[k];
-  }
-  // item o of u: token o / (R / 4), ranks 4 (o % (R / 4)) ..
-  __device__ __forceinline__ static int token(const Q8LoraArgs &a, int o) {
-    return (int)((uint32_t)o * (262144u / (uint32_t)a.R + 1) >> 16);  // (exact: o < 2^11, R / 4 <= 32)
-  }
-
-  // q: results (channels n ..) of token t
-  __device__ __forceinline__ void ask(const Q8LoraArgs &a, int q, int n) {
-    const int e = (uint32_t)id[q] < (uint32_t)a.L ? id[q] : 0;
-    scale[q] = a.scale ? a.scale[e] : 1.f;
-#pragma unroll
-    for (int p = 0; p < FIRST; ++p)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) piece(w[q][p][r], row(a, e, n + r) + min(8 * p, a.R - 8));
-  }
-  __device__ __forceinline__ static const T *row(const Q8LoraArgs &a, int e, int n) {
-    return static_cast<const T *>(a.b) + ((int64_t)e * a.N + min(n, a.N - 1)) * a.R;
-  }
-  __device__ __forceinline__ void ask_u(const Q8LoraArgs &a, int t0, int n) {
-    const int o = threadIdx.x, t = token(a, o);
-    if (t < n) part.load(a, t0 + t, 4 * o - t * a.R);
-  }
-  __device__ __forceinline__ void put_u(const Q8LoraArgs &a, int t0, int n, float *us) {
-    for (int o = threadIdx.x; token(a, o) < n; o += NT) {
-      const int t = token(a, o), r = 4 * o - t * a.R;
-      if (o != (int)threadIdx.x) part.load(a, t0 + t, r);
-      *reinterpret_cast<Pack<float, 4> *>(us + t * (a.R + 4) + r) = part.sum(a);
-    }
-  }
-  __device__ __forceinline__ void add(const Q8LoraArgs &a, int q, int n, const float *u, float *d) const {
-    if ((uint32_t)id[q] >= (uint32_t)a.L) return;
-    float l[4] = {0.f, 0.f, 0.f, 0.f};
-    auto mul = [&](int p, int r, const Pack<T, N> *x) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) l[r] = fmaf(u[8 * p + k], (float)x[k / N].v[k % N], l[r]);
-    };
-#pragma unroll
-    for (int p = 0; p < FIRST; ++p)
-      if (8 * p < a.R) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) mul(p, r, w[q][p][r]);
-      }
-    for (int p = FIRST; 8 * p < a.R; ++p) {
-      Pack<T, N> x[4][8 / N];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) piece(x[r], row(a, id[q], n + r) + 8 * p);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) mul(p, r, x[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) d[r] = fmaf(scale[q], l[r], d[r]);
-  }
-};
-
 // Bfloat16 pieces of u for a type's results.  They lie [32 positions][16 ranks]
 // [piece][lane][8]: lane l has position l % 32 and ranks 8 (l / 32) .. of the 16.
 constexpr int u_pieces(int dt) { return dt == COLI_F32 ? 3 : 2; }
@@ -152,6 +79,186 @@ __device__ __forceinline__ void split8(const float *v, v8bf *o) {
   split<P, 8>(v, o);
 }
 
+// Bfloat16 pieces of an adapter's element: fp16's 11 bits are two whole, fp32's 24
+// three.
+constexpr int b_pieces(int dt) { return dt == COLI_BF16 ? 1 : dt == COLI_F16 ? 2 : 3; }
+
+// The operand of ranks 8 p .. 8 p + 7 of a row of b in LDS, whose 16-byte piece h
+// lies at place(h); zero if not `in`.
+template <int DT, typename F>
+__device__ __forceinline__ void b_operand(const unsigned char *row, F place, int p, bool in, v8bf *w) {
+  typedef typename Elem<DT>::type T;
+  constexpr int N = 16 / (int)sizeof(T);
+  if constexpr (b_pieces(DT) == 1) {
+    w[0] = *reinterpret_cast<const v8bf *>(row + place(p));
+    w[0] = in ? w[0] : v8bf{};
+  } else {
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 8 / N; ++h) {
+      const Pack<T, N> x = *reinterpret_cast<const Pack<T, N> *>(row + place(8 / N * p + h));
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[h * N + k] = in ? (float)x.v[k] : 0.f;
+    }
+    split8<b_pieces(DT)>(v, w);
+  }
+}
+
+// Adds the adapters' part to the biases of the 16 x 16 results that a wave of
+// k_q8_ring finishes, by matrix instructions.  With few tokens nearly every one has
+// an adapter of its own, and the work is reading it: each wave brings the rows of b
+// for its 16 channels of one adapter of its 16 tokens after another, which lie
+// together, as whole lines into LDS of its own, D of them on the way, without a
+// barrier.  (Each lane reading its own token's rows into registers: 300 x 4000 of
+// rank 16, 64 and 128 45, 97 and 159 us, MEASURE so.)  u's parts are added, cut
+// into bfloat16 pieces and put in LDS for all the waves before.  Ranks go by chunks
+// of 128 bytes of b's rows.  Lane (li, lg) has channels 4 lg .. of token li, and
+// takes its own adapter's results and no other's, whatever they hold.
+template <int DT, int BM, int NT, int TPW, int LDS>
+struct LoraRing {
+  typedef typename Elem<DT>::type T;
+  static constexpr int PB = b_pieces(DT), PU = u_pieces(DT);
+  static constexpr int KC = 128 / (int)sizeof(T), UP = KC / 8;  // ranks of a chunk, and eighths of them
+  static constexpr int UPLANE = BM * UP * 16, BBUF = 2048;
+  static constexpr int ROOM = (LDS - PU * UPLANE) / (NT / 64) / BBUF, D = ROOM < 4 ? ROOM : 4;
+  static_assert(D >= 2, "buffers of b");
+  int id[TPW];
+  float scale[TPW], sum[TPW][4];
+  UParts<lora_parts(BM)> part;
+
+  __device__ __forceinline__ static int uplace(int row, int p) {
+    return (row * UP + (p ^ (UP == 8 ? row >> 1 & 7 : row >> 2 & 3))) * 16;
+  }
+  // place of piece p of row `row` of b, rows of pc pieces of 16 bytes
+  __device__ __forceinline__ static int bplace(int row, int p, int pc) {
+    return row * pc + (pc == 8 ? p ^ (row >> 1 & 7) : pc == 4 ? p ^ (row >> 2 & 3) : p);
+  }
+
+  // this thread's first share of u, asked for ahead
+  __device__ __forceinline__ void ask_u(const Q8LoraArgs &a, int t0, int n) {
+    const int t = threadIdx.x / (KC / 4), r = threadIdx.x % (KC / 4) * 4;
+    if (t < n && r < a.R) part.load(a, t0 + t, r);
+#pragma unroll
+    for (int q = 0; q < TPW; ++q) {
+      scale[q] = a.scale && (uint32_t)id[q] < (uint32_t)a.L ? a.scale[id[q]] : 1.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[q][k] = 0.f;
+    }
+  }
+  // u's pieces of the chunk from rank c on, zero from R to a multiple of 32
+  __device__ __forceinline__ void put_u(const Q8LoraArgs &a, int t0, int n, int c, unsigned char *lds) {
+    for (int o = threadIdx.x; o < n * (KC / 4); o += NT) {
+      const int t = o / (KC / 4), r = c + o % (KC / 4) * 4;
+      if (r >= ((a.R + 31) & ~31)) continue;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < a.R) {
+        if (c > 0 || o != (int)threadIdx.x) part.load(a, t0 + t, r);
+        const Pack<float, 4> s = part.sum(a);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = s.v[k];
+      }
+      v4bf u[PU];
+      split<PU, 4>(v, u);
+#pragma unroll
+      for (int p = 0; p < PU; ++p)
+        *reinterpret_cast<v4bf *>(lds + p * UPLANE + uplace(t, (r - c) / 8) + r % 8 * 2) = u[p];
+    }
+  }
+  // results q: 16 channels from n on, tokens row .. row + 15 of the tile
+  template <int NI>
+  __device__ __forceinline__ void mul(const Q8LoraArgs &a, int q, int row, int n, int c, unsigned char *lds) {
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int pc = min(8, (a.R - c) * (int)sizeof(T) / 16);
+    uint32_t off[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int slot = min(i * 64 + lane, 16 * pc - 1), r = slot * (65536 / pc + 1) >> 16;
+      off[i] = (uint32_t)(min(n + r, a.N - 1) - n) * (uint32_t)a.R * (uint32_t)sizeof(T) +
+               16 * (bplace(r, slot - r * pc, pc) - r * pc);
+    }
+    const char *b0 = static_cast<const char *>(a.b) + ((int64_t)n * a.R + c) * (int64_t)sizeof(T);
+    unsigned char *mine = lds + PU * UPLANE + wave * D * BBUF;
+    const uint32_t tokens = (uint32_t)__ballot((uint32_t)id[q] < (uint32_t)a.L) & 0xFFFF;
+    uint32_t ask = tokens, todo = tokens;
+    auto next = [&](uint32_t &m) {  // the first token's adapter; its tokens leave m
+      const int e = __builtin_amdgcn_readlane(id[q], __builtin_ctz(m));
+      m &= ~(uint32_t)__ballot(id[q] == e);
+      return e;
+    };
+    int at = 0;  // buffer
+    auto issue = [&](int to) {
+      const char *p = b0 + (int64_t)next(ask) * a.N * a.R * (int64_t)sizeof(T);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        __builtin_amdgcn_global_load_lds(p + off[i], (__attribute__((address_space(3))) void *)(mine + to * BBUF + i * 1024),
+                                         16, 0, 0);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (ask) issue(d);
+    while (todo) {
+      // the oldest buffer's rows are there: all but the others' loads have come
+      const bool more = ask != 0;
+      if (more) lds_wait<(D - 1) * NI>();
+      else lds_wait<0>();
+      const int e = next(todo);
+      const unsigned char *buf = mine + at * BBUF;
+      v4f l{0.f, 0.f, 0.f, 0.f};
+      const int steps = (min(KC, a.R - c) + 31) / 32;
+      for (int s = 0; s < steps; ++s) {
+        const int p = 4 * s + lg;
+        v8bf u[PU], w[PB];
+#pragma unroll
+        for (int k = 0; k < PU; ++k)
+          u[k] = *reinterpret_cast<const v8bf *>(lds + k * UPLANE + uplace(row + li, p));
+        b_operand<DT>(buf, [&](int h) { return 16 * bplace(li, h, pc); }, p, c + 8 * p < a.R, w);
+#pragma unroll
+        for (int k = 0; k < PB; ++k)
+#pragma unroll
+          for (int m = 0; m < PU; ++m)
+            if (k + m < (PB > PU ? PB : PU)) l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[k], u[m], l, 0, 0, 0);
+      }
+      if (id[q] == e) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[q][k] += l[k];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer has been read
+      if (more) issue(at);
+      at = at + 1 == D ? 0 : at + 1;
+    }
+  }
+  // s_waitcnt vmcnt(N)
+  template <int N>
+  __device__ __forceinline__ static void lds_wait() {
+    static_assert(N >= 0 && N < 16, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  }
+
+  // lds may hold what other waves have still to read until the first barrier
+  template <typename ROW, typename CHANNEL>
+  __device__ __forceinline__ void add(const Q8LoraArgs &a, int t0, int n, ROW row, CHANNEL channel, unsigned char *lds,
+                                      float (*d)[4]) {
+    for (int c = 0; c < a.R; c += KC) {
+      __syncthreads();
+      put_u(a, t0, n, c, lds);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < TPW; ++q) {
+        if (row(q) < 0 || row(q) >= n || channel(q) >= a.N) continue;
+        if ((a.R - c) * (int)sizeof(T) <= 64) mul<1>(a, q, row(q), channel(q), c, lds);
+        else mul<2>(a, q, row(q), channel(q), c, lds);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < TPW; ++q)
+      if ((uint32_t)id[q] < (uint32_t)a.L) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[q][k] = fmaf(scale[q], sum[q][k], d[q][k]);
+      }
+  }
+};
+
 // The adapters' part of a tile of k_q8_tile, by matrix instructions, after its
 // sums: for each group of 32 tokens one adapter of the group after another.  The
 // tile's tokens are in order of their adapters, so a group has few of them.  u
@@ -171,7 +278,7 @@ template <int DT, int BM, int BN, int WM, int WN>
 struct LoraTile {
   typedef typename Elem<DT>::type T;
   static constexpr int TN = BN / WN / 32;
-  static constexpr int PB = DT == COLI_BF16 ? 1 : DT == COLI_F16 ? 2 : 3, PU = u_pieces(DT);
+  static constexpr int PB = b_pieces(DT), PU = u_pieces(DT);
   static constexpr int N = 16 / (int)sizeof(T), H = 8 / N;  // elements and words of an eighth of ranks
   static constexpr int CS = H == 1 ? 4 : 2;                 // steps of 16 ranks asked for together
 

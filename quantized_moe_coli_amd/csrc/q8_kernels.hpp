@@ -190,8 +190,7 @@ struct RingKernel {
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   static constexpr int STEPS = 4 / KS;      // steps of k = 64 of a wave in a stage
   static constexpr int PART = KS * BM * BN * 4;
-  static constexpr int AFTER = PART + (LORA ? BM * (128 + 4) * 4 : 0);  // what takes the ring's place at the end
-  static constexpr int LDS = STAGES * STAGE > AFTER ? STAGES * STAGE : AFTER;
+  static constexpr int LDS = STAGES * STAGE > PART ? STAGES * STAGE : PART;
   static_assert(ROWS % (4 * NW) == 0 && BM % 4 == 0 && 4 % KS == 0, "whole loads and steps");
 
   __device__ __forceinline__ static void run(const ARGS &a, const Tile &t, unsigned char *ring,
@@ -248,7 +247,7 @@ struct RingKernel {
         bn[q][r] = a.bias ? a.bias[nr] : 0.f;
       }
     }
-    typename std::conditional<LORA, LoraRing<DT, BM, 64 * NW, TPW>, int>::type lo;
+    typename std::conditional<LORA, LoraRing<DT, BM, 64 * NW, TPW, LDS>, int>::type lo;
     if constexpr (LORA) {
 #pragma unroll
       for (int q = 0; q < TPW; ++q) lo.id[q] = a.ids[orow[q]];
@@ -307,18 +306,13 @@ struct RingKernel {
     };
     if constexpr (LORA) {
       for (; c + STAGES - 1 < stages; ++c) stage();
-      // (loads behind the stages': no wait for those counts too few)
-#pragma unroll
-      for (int q = 0; q < TPW; ++q) lo.ask(a, q, n0 + (min(q * NW + wave, TILES - 1) % (BN / 16)) * 16 + 4 * lg);
-      lo.ask_u(a, t.r0, t.n);
+      lo.ask_u(a, t.r0, t.n);  // (loads behind the stages': no wait for those counts too few)
       keep_order();
     }
     for (; c < stages; ++c) stage();
 
     stage_barrier<0>();
     int *part = reinterpret_cast<int *>(ring);
-    float *us = reinterpret_cast<float *>(ring + PART);
-    if constexpr (LORA) lo.put_u(a, t.r0, t.n, us);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -327,6 +321,18 @@ struct RingKernel {
         *reinterpret_cast<v4i *>(part + (kq * TILES + tl) * 256 + 4 * lane) = acc[i][j];
       }
     __syncthreads();
+    v4i sums[TPW];
+#pragma unroll
+    for (int q = 0; q < TPW; ++q) {
+      const int tl = min(q * NW + wave, TILES - 1);
+      sums[q] = *reinterpret_cast<const v4i *>(part + tl * 256 + 4 * lane);
+#pragma unroll
+      for (int k = 1; k < KS; ++k)
+        sums[q] += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
+    }
+    if constexpr (LORA)
+      lo.add(a, t.r0, t.n, [&](int q) { return q * NW + wave < TILES ? (q * NW + wave) / (BN / 16) * 16 : -1; },
+             [&](int q) { return n0 + (q * NW + wave) % (BN / 16) * 16; }, ring, bn);
     T *y = static_cast<T *>(a.y);
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(T)) == 0 && a.ldy % 4 == 0;
 #pragma unroll
@@ -334,14 +340,9 @@ struct RingKernel {
       const int tl = q * NW + wave;
       const int tt = (tl / (BN / 16)) * 16 + li, n = n0 + (tl % (BN / 16)) * 16 + 4 * lg;
       if (tl >= TILES || tt >= t.n || n >= a.N || orow[q] < 0) continue;
-      v4i sum = *reinterpret_cast<const v4i *>(part + tl * 256 + 4 * lane);
-#pragma unroll
-      for (int k = 1; k < KS; ++k)
-        sum += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
       Pack<T, 4> v;
-      if constexpr (LORA) lo.add(a, q, n, us + tt * (a.R + 4), bn[q]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(sum[r], st[q], sn[q][r], bn[q][r]);
+      for (int r = 0; r < 4; ++r) v.v[r] = (T)finish(sums[q][r], st[q], sn[q][r], bn[q][r]);
       T *d = y + (int64_t)orow[q] * a.ldy + n;
       if (vec && n + 4 <= a.N) {
         *reinterpret_cast<Pack<T, 4> *>(d) = v;

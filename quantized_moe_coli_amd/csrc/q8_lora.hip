@@ -13,9 +13,7 @@
 namespace coli {
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 // The 16 bytes of one row that a lane gives to a product, and 16 rows x 16 rows
 // over the 64 bytes of k that four lanes have of each row (lane l's are those of
