@@ -119,9 +119,8 @@ struct LoraRing {
   typedef typename Elem<DT>::type T;
   static constexpr int PB = b_pieces(DT), PU = u_pieces(DT);
   static constexpr int KC = 128 / (int)sizeof(T), UP = KC / 8;  // ranks of a chunk, and eighths of them
-  static constexpr int UPLANE = BM * UP * 16, BBUF = 2048;
-  static constexpr int ROOM = (LDS - PU * UPLANE) / (NT / 64) / BBUF, D = ROOM < 4 ? ROOM : 4;
-  static_assert(D >= 2, "buffers of b");
+  static constexpr int UPLANE = BM * UP * 16;
+  static constexpr int ROOM = (LDS - PU * UPLANE) / (NT / 64) / 1024;  // KB of b for a wave
   int id[TPW];
   float scale[TPW], sum[TPW][4];
   UParts<lora_parts(BM)> part;
@@ -164,9 +163,15 @@ struct LoraRing {
         *reinterpret_cast<v4bf *>(lds + p * UPLANE + uplace(t, (r - c) / 8) + r % 8 * 2) = u[p];
     }
   }
-  // results q: 16 channels from n on, tokens row .. row + 15 of the tile
+  // Results q: 16 channels from n on, tokens row .. row + 15 of the tile.  An
+  // adapter's rows are NI KB.  G adapters are multiplied together, so that one's
+  // wait for LDS is the other's too, and D are on the way.
   template <int NI>
   __device__ __forceinline__ void mul(const Q8LoraArgs &a, int q, int row, int n, int c, unsigned char *lds) {
+    // (as many as leave the registers for two workgroups a CU)
+    constexpr int FIT = ROOM / NI, MOST = NT <= 256 ? 4 : TPW > 1 || PB > 1 ? 2 : 3;
+    constexpr int G = FIT / 2 < MOST ? FIT / 2 : MOST, D = FIT / G < 3 ? FIT / G * G : 3 * G;
+    static_assert(G >= 1 && D >= 2 * G && (D - G) * NI < 16, "buffers of b");
     const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int pc = min(8, (a.R - c) * (int)sizeof(T) / 16);
@@ -178,7 +183,7 @@ struct LoraRing {
                16 * (bplace(r, slot - r * pc, pc) - r * pc);
     }
     const char *b0 = static_cast<const char *>(a.b) + ((int64_t)n * a.R + c) * (int64_t)sizeof(T);
-    unsigned char *mine = lds + PU * UPLANE + wave * D * BBUF;
+    unsigned char *mine = lds + PU * UPLANE + wave * ROOM * 1024;
     const uint32_t tokens = (uint32_t)__ballot((uint32_t)id[q] < (uint32_t)a.L) & 0xFFFF;
     uint32_t ask = tokens, todo = tokens;
     auto next = [&](uint32_t &m) {  // the first token's adapter; its tokens leave m
@@ -186,46 +191,57 @@ struct LoraRing {
       m &= ~(uint32_t)__ballot(id[q] == e);
       return e;
     };
-    int at = 0;  // buffer
     auto issue = [&](int to) {
       const char *p = b0 + (int64_t)next(ask) * a.N * a.R * (int64_t)sizeof(T);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        __builtin_amdgcn_global_load_lds(p + off[i], (__attribute__((address_space(3))) void *)(mine + to * BBUF + i * 1024),
+        __builtin_amdgcn_global_load_lds(p + off[i], (__attribute__((address_space(3))) void *)(mine + (to * NI + i) * 1024),
                                          16, 0, 0);
     };
 #pragma unroll
     for (int d = 0; d < D; ++d)
       if (ask) issue(d);
-    while (todo) {
-      // the oldest buffer's rows are there: all but the others' loads have come
-      const bool more = ask != 0;
-      if (more) lds_wait<(D - 1) * NI>();
+    const int steps = (min(KC, a.R - c) + 31) / 32;
+    for (int at = 0; todo; at = at + G == D ? 0 : at + G) {
+      // the oldest G are there: all but the others' loads have come
+      if (ask) lds_wait<(D - G) * NI>();
       else lds_wait<0>();
-      const int e = next(todo);
-      const unsigned char *buf = mine + at * BBUF;
-      v4f l{0.f, 0.f, 0.f, 0.f};
-      const int steps = (min(KC, a.R - c) + 31) / 32;
+      int e[G];
+      v4f l[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        e[g] = todo ? next(todo) : -1;
+        l[g] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+      const unsigned char *buf = mine + at * NI * 1024;
       for (int s = 0; s < steps; ++s) {
         const int p = 4 * s + lg;
-        v8bf u[PU], w[PB];
+        v8bf u[PU], w[G][PB];
 #pragma unroll
         for (int k = 0; k < PU; ++k)
           u[k] = *reinterpret_cast<const v8bf *>(lds + k * UPLANE + uplace(row + li, p));
-        b_operand<DT>(buf, [&](int h) { return 16 * bplace(li, h, pc); }, p, c + 8 * p < a.R, w);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          b_operand<DT>(buf + g * NI * 1024, [&](int h) { return 16 * bplace(li, h, pc); }, p, c + 8 * p < a.R, w[g]);
 #pragma unroll
         for (int k = 0; k < PB; ++k)
 #pragma unroll
           for (int m = 0; m < PU; ++m)
-            if (k + m < (PB > PU ? PB : PU)) l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[k], u[m], l, 0, 0, 0);
-      }
-      if (id[q] == e) {
+            if (k + m < (PB > PU ? PB : PU))
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum[q][k] += l[k];
+              for (int g = 0; g < G; ++g)
+                l[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[g][k], u[m], l[g], 0, 0, 0);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer has been read
-      if (more) issue(at);
-      at = at + 1 == D ? 0 : at + 1;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (e[g] >= 0 && id[q] == e[g]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[q][k] += l[g][k];
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffers have been read
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (ask) issue(at + g);
     }
   }
   // s_waitcnt vmcnt(N)
