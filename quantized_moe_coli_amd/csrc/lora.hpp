@@ -134,9 +134,9 @@ struct LoraRing {
   }
 
   // this thread's first share of u, asked for ahead
-  __device__ __forceinline__ void ask_u(const Q8LoraArgs &a, int t0, int n) {
+  __device__ __forceinline__ void ask_u(const Q8LoraArgs &a, const int *rows, int n) {
     const int t = threadIdx.x / (KC / 4), r = threadIdx.x % (KC / 4) * 4;
-    if (t < n && r < a.R) part.load(a, t0 + t, r);
+    if (t < n && r < a.R) part.load(a, max(rows[t], 0), r);
 #pragma unroll
     for (int q = 0; q < TPW; ++q) {
       scale[q] = a.scale && (uint32_t)id[q] < (uint32_t)a.L ? a.scale[id[q]] : 1.f;
@@ -145,13 +145,13 @@ struct LoraRing {
     }
   }
   // u's pieces of the chunk from rank c on, zero from R to a multiple of 32
-  __device__ __forceinline__ void put_u(const Q8LoraArgs &a, int t0, int n, int c, unsigned char *lds) {
+  __device__ __forceinline__ void put_u(const Q8LoraArgs &a, const int *rows, int n, int c, unsigned char *lds) {
     for (int o = threadIdx.x; o < n * (KC / 4); o += NT) {
       const int t = o / (KC / 4), r = c + o % (KC / 4) * 4;
       if (r >= ((a.R + 31) & ~31)) continue;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       if (r < a.R) {
-        if (c > 0 || o != (int)threadIdx.x) part.load(a, t0 + t, r);
+        if (c > 0 || o != (int)threadIdx.x) part.load(a, max(rows[t], 0), r);
         const Pack<float, 4> s = part.sum(a);
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = s.v[k];
@@ -253,11 +253,11 @@ struct LoraRing {
 
   // lds may hold what other waves have still to read until the first barrier
   template <typename ROW, typename CHANNEL>
-  __device__ __forceinline__ void add(const Q8LoraArgs &a, int t0, int n, ROW row, CHANNEL channel, unsigned char *lds,
+  __device__ __forceinline__ void add(const Q8LoraArgs &a, const int *rows, int n, ROW row, CHANNEL channel, unsigned char *lds,
                                       float (*d)[4]) {
     for (int c = 0; c < a.R; c += KC) {
       __syncthreads();
-      put_u(a, t0, n, c, lds);
+      put_u(a, rows, n, c, lds);
       __syncthreads();
 #pragma unroll
       for (int q = 0; q < TPW; ++q) {

@@ -213,7 +213,7 @@ struct RingKernel {
       pl[i] = (lane & 15) ^ (r & 15);
       if ((i * NW + wave) * 4 < BM) {
         const int tt = min(r, t.n - 1);
-        const int row = GROUPED ? in_row<GROUPED>(a, rows[tt]) : t.r0 + tt;
+        const int row = GROUPED ? in_row<GROUPED>(a, rows[tt]) : LORA ? max(rows[tt], 0) : t.r0 + tt;
         src[i] = reinterpret_cast<const uint8_t *>(a.q) + (size_t)row * a.K;
       } else {
         src[i] = a.w + ((size_t)t.e * a.N + min(n0 + r - BM, a.N - 1)) * a.K;
@@ -238,8 +238,8 @@ struct RingKernel {
     for (int q = 0; q < TPW; ++q) {
       const int tl = min(q * NW + wave, TILES - 1);
       const int tt = min((tl / (BN / 16)) * 16 + li, t.n - 1), n = n0 + (tl % (BN / 16)) * 16 + 4 * lg;
-      orow[q] = GROUPED ? rows[tt] : t.r0 + tt;
-      st[q] = a.s[in_row<GROUPED>(a, orow[q])];
+      orow[q] = GROUPED || LORA ? rows[tt] : t.r0 + tt;
+      st[q] = a.s[LORA ? max(orow[q], 0) : in_row<GROUPED>(a, orow[q])];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int nr = min(n + r, a.N - 1);
@@ -250,7 +250,7 @@ struct RingKernel {
     typename std::conditional<LORA, LoraRing<DT, BM, 64 * NW, TPW, LDS>, int>::type lo;
     if constexpr (LORA) {
 #pragma unroll
-      for (int q = 0; q < TPW; ++q) lo.id[q] = a.ids[orow[q]];
+      for (int q = 0; q < TPW; ++q) lo.id[q] = orow[q] < 0 ? -1 : a.ids[orow[q]];
     }
     keep_order();
 
@@ -306,7 +306,7 @@ struct RingKernel {
     };
     if constexpr (LORA) {
       for (; c + STAGES - 1 < stages; ++c) stage();
-      lo.ask_u(a, t.r0, t.n);  // (loads behind the stages': no wait for those counts too few)
+      lo.ask_u(a, rows, t.n);  // (loads behind the stages': no wait for those counts too few)
       keep_order();
     }
     for (; c < stages; ++c) stage();
@@ -331,7 +331,7 @@ struct RingKernel {
         sums[q] += *reinterpret_cast<const v4i *>(part + (k * TILES + tl) * 256 + 4 * lane);
     }
     if constexpr (LORA)
-      lo.add(a, t.r0, t.n, [&](int q) { return q * NW + wave < TILES ? (q * NW + wave) / (BN / 16) * 16 : -1; },
+      lo.add(a, rows, t.n, [&](int q) { return q * NW + wave < TILES ? (q * NW + wave) / (BN / 16) * 16 : -1; },
              [&](int q) { return n0 + (q * NW + wave) % (BN / 16) * 16; }, ring, bn);
     T *y = static_cast<T *>(a.y);
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(T)) == 0 && a.ldy % 4 == 0;
@@ -359,8 +359,12 @@ template <int DT, int BM, int BN, int WM, int WN, int KS, int STAGES, bool GROUP
 // (with adapters the larger ones would not leave the registers for two workgroups a CU)
 __global__ __launch_bounds__(64 * WM * WN * KS, kLora<ARGS> && WM * WN * KS == 8 ? 4 : 1) void k_q8_ring(ARGS a, int nbm, int nbn) {
   typedef RingKernel<DT, BM, BN, WM, WN, KS, STAGES, GROUPED, ARGS> K;
-  __shared__ __align__(16) unsigned char ring[K::LDS];
-  __shared__ int rows[GROUPED ? BM : 1];
+  // (With adapters the rows lie behind the ring, in one object with it: beside
+  // another object the compiler waits for every load into the ring before it reads
+  // it.)
+  __shared__ __align__(16) unsigned char ring[K::LDS + (kLora<ARGS> ? BM * 4 : 0)];
+  __shared__ int table[GROUPED ? BM : 1];
+  int *rows = kLora<ARGS> ? reinterpret_cast<int *>(ring + K::LDS) : table;
   Tile t;
   if constexpr (GROUPED) {
     t = expert_tile<BM>(a, nbn);
@@ -372,6 +376,13 @@ __global__ __launch_bounds__(64 * WM * WN * KS, kLora<ARGS> && WM * WN * KS == 8
     if (id < 0) return;
     const int m = id % nbm;  // the token tiles of a channel block are neighbours
     t = Tile{0, m * BM, min(BM, a.rows - m * BM), id / nbm};
+    if constexpr (kLora<ARGS>) {
+      if ((int)threadIdx.x < t.n) {
+        const int row = a.order ? a.order[t.r0 + threadIdx.x].x : t.r0 + threadIdx.x;
+        rows[threadIdx.x] = (uint32_t)row < (uint32_t)a.rows ? row : -1;
+      }
+      __syncthreads();
+    }
   }
   K::run(a, t, ring, rows);
 }

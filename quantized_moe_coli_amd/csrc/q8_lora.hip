@@ -184,8 +184,10 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   constexpr int ASYNC = VEC ? NL : NL - TM;    // of them straight to LDS
   static_assert(STAGES >= 3 && STAGES * STAGE >= NW * RT * 1024, "the sums take the ring's place");
   static_assert(ASYNC * (STAGES - 1) < 64, "vmcnt range");
-  __shared__ __align__(16) unsigned char ring[STAGES * STAGE];
-  __shared__ int rows[BM < 32 ? 32 : BM];
+  // (The rows lie behind the ring, in one object with it: beside another object the
+  // compiler waits for every load into the ring before it reads it.)
+  __shared__ __align__(16) unsigned char ring[STAGES * STAGE + (BM < 32 ? 32 : BM) * 4];
+  int *rows = reinterpret_cast<int *>(ring + STAGES * STAGE);
   if ((int)blockIdx.x >= wgs) {
     order_tokens<NW>(g, blockIdx.x - wgs, rows);
     return;
@@ -338,7 +340,8 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
   const int tiles = one ? a.rows : a.rows / bm + std::min(a.rows, a.L);  // at most
   a.slices = a.pieces ? 1 : slices_of(a.rows, one ? a.rows : (a.rows + bm - 1) / bm, lora_parts(kShapes[v].bm));
   const int wgs = (int)(((int64_t)tiles * a.slices + 7) / 8 * 8);
-  const int extra = a.pieces ? (a.rows + kOrder - 1) / kOrder : 0;
+  const int extra = (a.rows + kOrder - 1) / kOrder;
+  if (one) a.order = nullptr;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;
     auto few = [&](auto vecc) {
