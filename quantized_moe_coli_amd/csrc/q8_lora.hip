@@ -160,28 +160,35 @@ __global__ __launch_bounds__(512) void k_lora_down_one(Q8LoraArgs g) {
 }
 
 // u of up to BM tokens of one adapter, over one of the slices of K, by matrix
-// instructions.  K goes by stages of 256 bytes of every row through a ring in LDS,
-// filled by direct loads of whole runs of four rows (16 rows' lines at one k, read
-// straight into operand registers, took 1.2 to 1.5 times as long).  Each of the four
-// waves has 64 of the 256 bytes of every row, and the waves' sums are added through
-// LDS in order.  RT groups of 16 ranks (rows past R repeat its last).
+// instructions.  K goes by stages of SB bytes of every row through a ring in LDS,
+// filled by direct loads of whole runs of rows.  A stage costs a barrier and a wait
+// for LDS whatever its size, so it is as long as three of them fit (509 tokens x
+// 6144 of rank 16: 256 bytes 12.6 us, 512 10.1, 1024 9.5).  Each of the four waves has every
+// fourth 64 bytes of a row, and the waves' sums are added through LDS in order.  RT
+// groups of 16 ranks (rows past R repeat its last).
 //
 // LDS: piece p (16 bytes) of row r's stage lies at place p ^ (r % 16).
 //
 // (Workgroups that each begin at another stage take 1.35 times as long: side by
 // side they read an adapter's a while it is near.)
+constexpr int down_bytes(int bm, int rt) {
+  return bm + 16 * rt <= 96 ? 512 : 256;
+}
 constexpr int down_stages(int bm, int rt) {
-  const int stage = (bm + 16 * rt) * 256, two = (78 << 10) / stage;  // two workgroups a CU
-  return two >= 3 ? (two < 8 ? two : 8) : (150 << 10) / stage;
+  const int n = (150 << 10) / ((bm + 16 * rt) * down_bytes(bm, rt));
+  return n < 6 ? n : 6;
 }
 
 template <int DT, bool VEC, int BM, int RT>
 __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   typedef typename Elem<DT>::type T;
   typedef typename Oper<DT>::type O;
-  constexpr int NW = 4, ROWS = BM + 16 * RT, STAGE = ROWS * 256, PIECES = 16, STAGES = down_stages(BM, RT);
-  constexpr int TM = BM / 16, NL = ROWS / 16;  // loads of a wave in a stage, the tokens' TM first
-  constexpr int ASYNC = VEC ? NL : NL - TM;    // of them straight to LDS
+  constexpr int NW = 4, SB = down_bytes(BM, RT), ROWS = BM + 16 * RT, STAGE = ROWS * SB, PIECES = SB / 16;
+  constexpr int STAGES = down_stages(BM, RT), KS = SB / 64 / NW;  // steps of a wave in a stage
+  constexpr int RPL = 1024 / SB;                                  // rows of a load
+  constexpr int TM = BM / 16;
+  constexpr int NX = BM / RPL / NW, NL = ROWS / RPL / NW;  // loads of a wave in a stage, the tokens' NX first
+  constexpr int ASYNC = VEC ? NL : NL - NX;                // of them straight to LDS
   static_assert(STAGES >= 3 && STAGES * STAGE >= NW * RT * 1024, "the sums take the ring's place");
   static_assert(ASYNC * (STAGES - 1) < 64, "vmcnt range");
   // (The rows lie behind the ring, in one object with it: beside another object the
@@ -212,9 +219,9 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   uint32_t pl[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    const int r = (i * NW + wave) * 4 + lane / 16;
-    pl[i] = (lane & 15) ^ (r & 15);
-    src[i] = i < TM ? static_cast<const char *>(g.x) + max(rows[r], 0) * g.ldx * (int64_t)sizeof(T)
+    const int r = (i * NW + wave) * RPL + lane / PIECES;
+    pl[i] = (lane & (PIECES - 1)) ^ (r & 15);
+    src[i] = i < NX ? static_cast<const char *>(g.x) + max(rows[r], 0) * g.ldx * (int64_t)sizeof(T)
                     : static_cast<const char *>(g.a) +
                           ((int64_t)t.e * g.R + min(r - BM, g.R - 1)) * g.K * (int64_t)sizeof(T);
   }
@@ -223,9 +230,9 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
     const uint32_t last = min(PIECES, pieces - PIECES * c) - 1;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const char *p = src[i] + (int64_t)c * 256 + 16 * min(pl[i], last);
+      const char *p = src[i] + (int64_t)c * SB + 16 * min(pl[i], last);
       unsigned char *to = buf + (i * NW + wave) * 1024;
-      if (VEC || i >= TM) {
+      if (VEC || i >= NX) {
         __builtin_amdgcn_global_load_lds(p, (lds_void *)to, 16, 0, 0);
       } else {  // rows that start at any element
         Pack<T, 16 / (int)sizeof(T)> v;
@@ -250,17 +257,22 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
     if (c + STAGES - 1 <= end) stage_barrier<ASYNC *(STAGES - 2)>();
     else stage_barrier<0>();
     if (c + STAGES - 1 < end) issue(c + STAGES - 1);
-    const unsigned char *buf = ring + ((c - first) % STAGES) * STAGE + li * 256 + 16 * ((4 * wave + lg) ^ li);
-    if (PIECES * c + 4 * wave >= pieces) continue;  // (pieces are a multiple of 4)
-    O x[TM], w[RT];
+    const unsigned char *buf = ring + ((c - first) % STAGES) * STAGE + li * SB;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) x[j] = *reinterpret_cast<const O *>(buf + 16 * j * 256);
+    for (int k = 0; k < KS; ++k) {
+      const int p = 4 * (k * NW + wave);
+      if (PIECES * c + p >= pieces) continue;  // (pieces are a multiple of 4)
+      const unsigned char *b = buf + 16 * ((p + lg) ^ li);
+      O x[TM], w[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const O *>(buf + (BM + 16 * i) * 256);
+      for (int j = 0; j < TM; ++j) x[j] = *reinterpret_cast<const O *>(b + 16 * j * SB);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const O *>(b + (BM + 16 * i) * SB);
 #pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[i], x[j], acc[i][j]);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = mul16<DT>(w[i], x[j], acc[i][j]);
+    }
   }
   // lane (li, lg) has token li's ranks 4 lg .. 4 lg + 3 of each 16
   float *part = reinterpret_cast<float *>(ring);
