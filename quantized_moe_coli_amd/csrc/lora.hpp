@@ -109,11 +109,14 @@ __device__ __forceinline__ void b_operand(const unsigned char *row, F place, int
 // an adapter of its own, and the work is reading it: each wave brings the rows of b
 // for its 16 channels of one adapter of its 16 tokens after another, which lie
 // together, as whole lines into LDS of its own, D of them on the way, without a
-// barrier.  (Each lane reading its own token's rows into registers: 300 x 4000 of
-// rank 16, 64 and 128 45, 97 and 159 us, MEASURE so.)  u's parts are added, cut
-// into bfloat16 pieces and put in LDS for all the waves before.  Ranks go by chunks
-// of 128 bytes of b's rows.  Lane (li, lg) has channels 4 lg .. of token li, and
-// takes its own adapter's results and no other's, whatever they hold.
+// barrier.  (300 tokens x 4000 channels x 6144 with 64 adapters of rank 16, 64 and
+// 128: 40, 51 and 72 us for both launches, with each lane reading its own token's
+// rows into registers 45, 97 and 159.  Asking for the rows' lines while the sums are
+// still made does not help: 28, 37 and 55 us instead of 28, 33 and 46 at 61 x 6144.)
+// u's parts are added, cut into bfloat16 pieces and put in LDS for all the waves
+// before.  Ranks go by chunks of 128 bytes of b's rows.  Lane (li, lg) has channels 4
+// lg .. of token li, and takes its own adapter's results and no other's, whatever
+// they hold.
 template <int DT, int BM, int NT, int TPW, int LDS>
 struct LoraRing {
   typedef typename Elem<DT>::type T;
@@ -290,6 +293,12 @@ struct LoraRing {
 // A lane's results are one token's: where a group has one adapter its products go
 // straight to the results, otherwise a token takes those of its own adapter and
 // none of another's, whatever they hold.
+//
+// 8192 x 6144 x 6144, launches of the product alone: 290 us where no token has an
+// adapter, 295 with one of rank 16, 306 with eight of rank 64, 323 with sixteen of
+// rank 128 (least of 12).  Each adapter of a group costs a wait for its rows, so
+// where a group has many they are what it waits for: 509 x 6144 x 6144 of rank 16 37
+// us with one, 45 with 64 in any order.
 template <int DT, int BM, int BN, int WM, int WN>
 struct LoraTile {
   typedef typename Elem<DT>::type T;

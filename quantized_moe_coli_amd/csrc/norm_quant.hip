@@ -13,7 +13,10 @@
 //
 // Bound by the memory: every element of x, res, h, y and q is moved once, as
 // long as a row fits the registers of the threads that share it; longer rows
-// (past 32768 elements) are read three times.
+// (past 32768 elements) are read three times.  8192 x 6144 bfloat16 with h, y and
+// codes 95.5 us (453 MB, 4.7 TB/s; a copy reaches 5.06), float32 with h and y 148 us
+// (5.4 TB/s); one row 4.4 us, of which a launch is 2, two sums over its workgroup
+// the most of the rest.
 #include <algorithm>
 #include <type_traits>
 
@@ -277,11 +280,16 @@ hipError_t launch_norm_quant(int dt, const NormArgs &a, hipStream_t st) {
       hipLaunchKernelGGL((k_norm_quant<DT, decltype(vecc)::value, TR, decltype(npc)::value>),
                          dim3(std::min(wgs, kGridX), (wgs + kGridX - 1) / kGridX), dim3(NT), 0, st, a);
     };
-    // few rows: a thread for every piece, the shortest way through a row
+    // Few rows: a thread for every piece, the shortest way through a row; many: four
+    // pieces a thread, more rows at a time.  With h, y and codes in bfloat16 (us, the one
+    // / the other):
+    //   512 columns:   256 rows 3.1 / 3.4, 1024 3.4 / 3.7, 4096 7.3 / 7.1
+    //   2048 columns:  256 rows 3.6 / 6.8, 1024 7.5 / 9.3, 4096 16.6 / 16.5
+    //   6144 columns:  16 rows 4.6 / 5.6, 256 6.2 / 7.3, 512 10.6 / 9.5, 4096 63.6 / 46.4
     auto by_len = [&](auto vecc) {
       constexpr std::integral_constant<int, 1> one{};
       constexpr std::integral_constant<int, 4> four{};
-      if (a.T <= 512) {
+      if (a.T <= (a.n <= 256 * kPiece ? 2048 : 384)) {
         if (a.n <= 16 * kPiece) go(vecc, std::integral_constant<int, 16>(), one);
         else if (a.n <= 64 * kPiece) go(vecc, std::integral_constant<int, 64>(), one);
         else if (a.n <= 256 * kPiece) go(vecc, std::integral_constant<int, 256>(), one);

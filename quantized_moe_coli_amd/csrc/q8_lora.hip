@@ -340,7 +340,7 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
                    (uint64_t)a.ldx * (dt == COLI_F32 ? 4 : 2) % 16 == 0;
   // Tokens of a tile: a tile costs its tokens' and its adapter's rows, and a CU
   // works through its tiles one after another.  (8192 x 6144 of rank 64, 16 adapters:
-  // 272 tiles of 32 tokens 52-56 us, 187 of 48 MEASURE.)
+  // 272 tiles of 32 tokens 52-56 us, 187 of 48 38-43.)
   int bm = 16;
   if (!one && vec) {
     int64_t least = INT64_MAX;

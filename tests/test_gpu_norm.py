@@ -93,7 +93,8 @@ def call(x, res=None, gain=None, codes=True, y=True, h=True, stream=None, eps=EP
     (2, 2048, 0, 0), (2, 2080, 0, 0), (1, 6144, 0, 0), (3, 8192, 8, 0), (2, 8224, 0, 0), (2, 32768, 0, 0),
     (1, 33024, 0, 0), (1, 131040, 0, 0), (4, 96, 5, 3), (2, 6176, 1, 1), (1, 40032, 3, 2),
     (513, 64, 0, 0), (514, 160, 0, 0), (600, 2048, 8, 0), (515, 2080, 0, 0), (520, 8224, 0, 0),
-    (513, 96, 5, 3)])
+    (513, 96, 5, 3), (2049, 64, 0, 0), (2053, 160, 0, 0), (2100, 2048, 8, 0), (2049, 512, 0, 0),
+    (2049, 96, 5, 3), (385, 2080, 0, 0)])
 def test_norm_codes(dt, T, n, pad, shift):
     x, res = rows(T, n, DT[dt], 1, pad, shift), rows(T, n, DT[dt], 2, pad, shift, 3.0)
     gain = (1 + 0.3 * torch.randn(n, generator=gen(n))).cuda()
@@ -102,7 +103,8 @@ def test_norm_codes(dt, T, n, pad, shift):
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("T,n", [(1, 1), (3, 2), (70, 7), (5, 9), (4, 127), (1021, 129), (9, 513), (700, 1001),
-                                 (2, 8191), (1, 8193), (2, 32773), (1, 131071), (1, 131072), (530, 33)])
+                                 (2, 8191), (1, 8193), (2, 32773), (1, 131071), (1, 131072), (530, 33),
+                                 (2051, 33), (2049, 1001), (2200, 513)])
 def test_norm_rows_of_any_length(dt, T, n):
     x, res = rows(T, n, DT[dt], 3), rows(T, n, DT[dt], 4, scale=2.0)
     gain = (1 + 0.3 * torch.randn(n, generator=gen(n, 1))).cuda()

@@ -31,7 +31,8 @@ def test_gemm_q8_lora():
     need = B.coli_lora_workspace_bytes(4, 16)
     refuse("coli_gemm_q8_lora", good, [dict(ws_=None), dict(ws_=P + 128), dict(wsn=need - 1), dict(wsn=0)],
            B.COLI_ERR_WORKSPACE)
-    refuse("coli_gemm_q8_lora", good, [dict(T=1 << 20, N=1 << 30, ldy=1 << 30, wsn=1 << 40)], UNSUPPORTED)
+    refuse("coli_gemm_q8_lora", good, [dict(T=1 << 20, N=1 << 30, ldy=1 << 30, wsn=1 << 40),
+                                       dict(T=1 << 16, K=1 << 16, ldx=1 << 16, N=6144, ldy=6144, wsn=1 << 40)], UNSUPPORTED)
     no_device_or_empty("coli_gemm_q8_lora", dict(good, wsn=need), dict(T=0, q=None, s=None, y=None, ws_=None, x=None))
 
 
