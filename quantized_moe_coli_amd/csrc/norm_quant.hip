@@ -283,23 +283,28 @@ hipError_t launch_norm_quant(int dt, const NormArgs &a, hipStream_t st) {
     // Few rows: a thread for every piece, the shortest way through a row; many: four
     // pieces a thread, more rows at a time.  With h, y and codes in bfloat16 (us, the one
     // / the other):
+    //   192 columns, 33564 rows, by 16 and by 64 threads 14.9 / 26.5; 512 x 4096 8.2 / 5.7
     //   512 columns:   256 rows 3.1 / 3.4, 1024 3.4 / 3.7, 4096 7.3 / 7.1
     //   2048 columns:  256 rows 3.6 / 6.8, 1024 7.5 / 9.3, 4096 16.6 / 16.5
     //   6144 columns:  16 rows 4.6 / 5.6, 256 6.2 / 7.3, 512 10.6 / 9.5, 4096 63.6 / 46.4
     auto by_len = [&](auto vecc) {
       constexpr std::integral_constant<int, 1> one{};
       constexpr std::integral_constant<int, 4> four{};
-      if (a.T <= (a.n <= 256 * kPiece ? 2048 : 384)) {
-        if (a.n <= 16 * kPiece) go(vecc, std::integral_constant<int, 16>(), one);
-        else if (a.n <= 64 * kPiece) go(vecc, std::integral_constant<int, 64>(), one);
+      // (1024 threads that load by elements have registers for one piece: 638 rows of
+      // 9952 33 us, with four, which are kept in memory, 1581)
+      constexpr std::integral_constant<int, decltype(vecc)::value ? 4 : 1> most{};
+      if (a.n <= 16 * kPiece) {
+        go(vecc, std::integral_constant<int, 16>(), one);
+      } else if (a.T <= (a.n <= 256 * kPiece ? 2048 : 384)) {
+        if (a.n <= 64 * kPiece) go(vecc, std::integral_constant<int, 64>(), one);
         else if (a.n <= 256 * kPiece) go(vecc, std::integral_constant<int, 256>(), one);
         else if (a.n <= 1024 * kPiece) go(vecc, std::integral_constant<int, 1024>(), one);
-        else go(vecc, std::integral_constant<int, 1024>(), four);
+        else go(vecc, std::integral_constant<int, 1024>(), most);
       } else {
-        if (a.n <= 16 * kPiece) go(vecc, std::integral_constant<int, 16>(), one);
+        if (a.n <= 16 * kPiece * 3) go(vecc, std::integral_constant<int, 16>(), four);
         else if (a.n <= 64 * kPiece * 4) go(vecc, std::integral_constant<int, 64>(), four);
         else if (a.n <= 256 * kPiece * 4) go(vecc, std::integral_constant<int, 256>(), four);
-        else go(vecc, std::integral_constant<int, 1024>(), four);
+        else go(vecc, std::integral_constant<int, 1024>(), most);
       }
     };
     if (vec) by_len(std::true_type());

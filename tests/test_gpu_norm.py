@@ -94,7 +94,8 @@ def call(x, res=None, gain=None, codes=True, y=True, h=True, stream=None, eps=EP
     (1, 33024, 0, 0), (1, 131040, 0, 0), (4, 96, 5, 3), (2, 6176, 1, 1), (1, 40032, 3, 2),
     (513, 64, 0, 0), (514, 160, 0, 0), (600, 2048, 8, 0), (515, 2080, 0, 0), (520, 8224, 0, 0),
     (513, 96, 5, 3), (2049, 64, 0, 0), (2053, 160, 0, 0), (2100, 2048, 8, 0), (2049, 512, 0, 0),
-    (2049, 96, 5, 3), (385, 2080, 0, 0)])
+    (2049, 96, 5, 3), (385, 2080, 0, 0),
+    (2061, 224, 0, 0), (2049, 384, 8, 0), (2052, 288, 7, 1), (386, 9952, 7, 0), (385, 9952, 0, 0)])
 def test_norm_codes(dt, T, n, pad, shift):
     x, res = rows(T, n, DT[dt], 1, pad, shift), rows(T, n, DT[dt], 2, pad, shift, 3.0)
     gain = (1 + 0.3 * torch.randn(n, generator=gen(n))).cuda()
