@@ -343,7 +343,8 @@ coli_status coli_moe_forward_noalloc(const coli_moe_layer *L, const float *x,
  * elements and at least the row's length; elements of a row are consecutive.
  * Rows that start 16-byte aligned are read and written in 16-byte words,
  * others element by element.  The calls need no workspace (coli_gemm_q8_lora
- * excepted), keep nothing and may be captured into a graph.  Buffers must not overlap unless stated.
+ * excepted), keep nothing and may be captured into a graph.  Buffers must not
+ * overlap unless stated.
  * ------------------------------------------------------------------------- */
 typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
 
@@ -378,10 +379,10 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
  * coli_quant_act_token makes them (so their operand is not y as it was rounded to
  * a 16-bit type).  Each output may be NULL: q and s together, and one of y_out
  * and q must be there.  h_out and y_out may be x or res themselves, with the same
- * row stride, but not one another.  A row holding a NaN or an infinity gets NaN
- * where it stands in y, s = NaN and q = 0.  eps finite and above 0; n at least 1 and
- * at most 131072, with q a multiple of 32 and at most 131040; 0 <= T <= 2^25 (a row
- * may be one head's). */
+ * row stride, but not one another.  A row whose h holds an infinity gets NaN where
+ * it stands in y and 0 elsewhere, one with a NaN gets NaN all along; s = NaN and
+ * q = 0 in both.  eps finite and above 0; n at least 1 and at most 131072, with q a
+ * multiple of 32 and at most 131040; 0 <= T <= 2^25 (a row may be one head's). */
 coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx,
                                      const void *res, int64_t ldres,
                                      const float *gain, float eps, int32_t T,

@@ -483,7 +483,7 @@ def coli_gemm_q8_lora(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor, ws: tor
                       bias: torch.Tensor | None = None, stream=None) -> None:
     """coli_gemm_q8 plus each token's adapter: q int8 [T, K], s fp32 [T], w uint8
     [N, K] int8 codes, ws fp32 [N], x [T, K] the activations of the codes (rows may
-    be strided), ids int32 [T] adapters (none outside [0, L)), offs int32 [L + 1] and
+    be strided), ids int32 [T] adapters (outside [0, L): no adapter), offs int32 [L + 1] and
     perm int32 [T] coli_moe_dispatch's tables of ids [T, 1], bias fp32 [N] or None ->
     y [T, N] (rows may be strided); x, y and the adapters of one float type.
     workspace as lora_workspace makes it, for one call at a time."""
