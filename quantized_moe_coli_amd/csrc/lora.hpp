@@ -290,9 +290,12 @@ struct LoraRing {
 // or 11 bits, three none.  Adapters in fp16 enter as two pieces, which hold them
 // whole, in fp32 as three.
 //
-// A lane's results are one token's: where a group has one adapter its products go
-// straight to the results, otherwise a token takes those of its own adapter and
-// none of another's, whatever they hold.
+// A lane's results are one token's: it takes those of its token's adapter and none of
+// another's, whatever they hold.  The products of up to CS steps are summed by
+// themselves and then added, one rounding at the result's size for 64 (bfloat16) or
+// 32 ranks.  (Products that go straight to the results round there in every matrix
+// instruction, 3 R / 8 of them in binary32: parts of an adapter that lie below half a
+// step of a large result were lost one by one.)
 //
 // 8192 x 6144 x 6144, launches of the product alone: 290 us where no token has an
 // adapter, 295 with one of rank 16, 306 with eight of rank 64, 323 with sixteen of
@@ -360,13 +363,11 @@ struct LoraTile {
       int held = -1;  // the adapter whose rows are in b
 #pragma unroll
       for (int j = 0; j < TMV; ++j) {
-        const int g0 = (j * WM + wm) * 32;
         uint64_t todo = __ballot(id[j] >= 0);
         if (todo) load_u(j, s0);
         while (todo) {
           const int e = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(todo));
           todo &= ~__ballot(id[j] == e);
-          const bool whole = __ballot(g0 + lr < n && id[j] != e) == 0;
           if (e != held) {
             const T *b0 = static_cast<const T *>(a.b) + ((int64_t)e * a.N + n0) * a.R;
 #pragma unroll
@@ -384,7 +385,7 @@ struct LoraTile {
           for (int i = 0; i < TN; ++i) {
             v16f l;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) l[r] = whole ? __int_as_float(acc[i][j][r]) : 0.f;
+            for (int r = 0; r < 16; ++r) l[r] = 0.f;
 #pragma unroll
             for (int s = 0; s < CS; ++s)
               if (s0 + s < steps) {
@@ -404,10 +405,9 @@ struct LoraTile {
                     if (p + q < (PB > PU ? PB : PU))
                       l = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[s][q], l, 0, 0, 0);
               }
-            if (whole || id[j] == e) {
+            if (id[j] == e) {
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
-                acc[i][j][r] = __float_as_int(whole ? l[r] : __int_as_float(acc[i][j][r]) + l[r]);
+              for (int r = 0; r < 16; ++r) acc[i][j][r] = __float_as_int(__int_as_float(acc[i][j][r]) + l[r]);
             }
           }
         }
