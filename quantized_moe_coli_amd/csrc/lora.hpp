@@ -59,9 +59,8 @@ constexpr int lora_parts(int bm) { return bm == 16 ? 8 : 4; }
 // [piece][lane][8]: lane l has position l % 32 and ranks 8 (l / 32) .. of the 16.
 constexpr int u_pieces(int dt) { return dt == COLI_F32 ? 3 : 2; }
 
-// v as a sum of P bfloat16 pieces, each the rounding of what is left: 8 bits a
-// piece and one more by the sign of the rest, so two hold 2^-18 of v, three all
-// of binary32.
+// v as a sum of P bfloat16 pieces, each the rounding of what is left, by at most half a
+// step of its 8 bits: one leaves up to 2^-8 of v, two 2^-17, three nothing of binary32.
 template <int P, int M, typename V>
 __device__ __forceinline__ void split(const float *v, V *o) {
 #pragma unroll
@@ -82,6 +81,11 @@ __device__ __forceinline__ void split8(const float *v, v8bf *o) {
 // Bfloat16 pieces of an adapter's element: fp16's 11 bits are two whole, fp32's 24
 // three.
 constexpr int b_pieces(int dt) { return dt == COLI_BF16 ? 1 : dt == COLI_F16 ? 2 : 3; }
+
+// Whether piece k of b's element is multiplied by piece m of u.  What is left out is up
+// to 2^-24 of the product in fp32 (k + m = 3: 2^-8 of one by 2^-17 of the other, twice)
+// and nothing in fp16, whose two low pieces would be 2^-16.
+constexpr bool pieces_meet(int k, int m) { return k + m < 3; }
 
 // The operand of ranks 8 p .. 8 p + 7 of a row of b in LDS, whose 16-byte piece h
 // lies at place(h); zero if not `in`.
@@ -230,7 +234,7 @@ struct LoraRing {
         for (int k = 0; k < PB; ++k)
 #pragma unroll
           for (int m = 0; m < PU; ++m)
-            if (k + m < (PB > PU ? PB : PU))
+            if (pieces_meet(k, m))
 #pragma unroll
               for (int g = 0; g < G; ++g)
                 l[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[g][k], u[m], l[g], 0, 0, 0);
@@ -286,7 +290,7 @@ struct LoraRing {
 // of 16 zero; b's rows go straight from memory to registers too (past R a row's last
 // ranks again, of which the result has its part already), without LDS or a barrier.
 //
-// u is a binary32 sum: two bfloat16 pieces lose 2^-18 of it where the result has 8
+// u is a binary32 sum: two bfloat16 pieces lose up to 2^-17 of it where the result has 8
 // or 11 bits, three none.  Adapters in fp16 enter as two pieces, which hold them
 // whole, in fp32 as three.
 //
@@ -402,7 +406,7 @@ struct LoraTile {
                 for (int p = 0; p < PB; ++p)
 #pragma unroll
                   for (int q = 0; q < PU; ++q)
-                    if (p + q < (PB > PU ? PB : PU))
+                    if (pieces_meet(p, q))
                       l = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p], u[s][q], l, 0, 0, 0);
               }
             if (id[j] == e) {
