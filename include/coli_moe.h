@@ -432,8 +432,10 @@ size_t coli_lora_workspace_bytes(int32_t max_tokens, int32_t rank);
  * coli_gemm_q8's, bit for bit.  x [T][K], row stride ldx, are the activations of
  * which q and s are the codes, in dtype like a, b and y.  ids [T] int32; offs
  * [L + 1] and perm [T] are coli_moe_dispatch's tables of ids as one slot a token
- * (k = 1, E = L), which one call makes for all projections of a batch; a token
- * that they list under another adapter, or not at all, gets an undefined row.
+ * (k = 1, E = L), which one call makes for all projections of a batch.  They list no
+ * token twice.  A token whose id is in [0, L) and that they list under another
+ * adapter, or not at all, gets an undefined row, and no other token's row changes for
+ * it; whether a token without an adapter is listed does not matter.
  * u is an fp32 sum, not rounded to a 16-bit type: it enters the second product to
  * 2^-17 of its value where dtype is one, and to 2^-24 in fp32.  The adapters'
  * part is summed by itself in fp32, whole or by 32 ranks or more, and joins the

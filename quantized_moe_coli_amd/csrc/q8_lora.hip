@@ -56,51 +56,124 @@ __device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int 
 }
 
 // The tokens in order of their adapters: the table's, and behind them, in order,
-// the tokens without one, which the table does not list.  Workgroup b writes the
-// table's part of positions kOrder b .. and the tokens without an adapter among
-// tokens kOrder b ..; those before them it counts itself.
+// the tokens without one, which the table does not list.  A table may be wrong about
+// a token (made from other ids): every position is written, by one thread, and names
+// no token that the table does not have right, so that nothing but that token's own
+// row is lost.  A position counts if it lies in the range of its token's adapter;
+// one that does not, and what is left at the end where tokens are not listed, names
+// none.  Where listed tokens and those without an adapter are more than there are,
+// some of these are listed: they keep the table's place and are passed over behind it.
+//
+// Workgroup b writes the table's part of positions kOrder b .. and the tokens without
+// an adapter among tokens kOrder b ..; those before and behind them it counts itself.
 constexpr int kOrder = 1024;
+constexpr int kMaxAdapters = 1024;
+constexpr int kOrderInts = 48 + kOrder / 32 + kMaxAdapters + 1;  // of LDS
 
 template <int NW>
-__device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *count) {
-  static_assert(NW <= 16 && kOrder % (64 * NW) == 0, "whole rounds");
+__device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *lds) {
+  static_assert(NW <= 16 && kOrder % (64 * NW) == 0 && kOrder <= 32 * 64 * NW, "whole rounds");
   constexpr int M = kOrder / 64 / NW;
+  // for each wave: tokens without an adapter before this workgroup's, its own, and behind
+  int *count = lds;
+  uint32_t *listed = reinterpret_cast<uint32_t *>(lds + 48);  // a bit for each of this workgroup's tokens
+  int *offs = lds + 48 + kOrder / 32;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
-  auto bare = [&](int t) { return t < g.rows && (uint32_t)g.ids[t] >= (uint32_t)g.L; };
-  int before = 0, mine = 0;  // (before: of this wave's share)
-  // (a run of eight loads at a time: t0 is a multiple of kOrder)
+  auto bare = [&](int e) { return (uint32_t)e >= (uint32_t)g.L; };
+  auto wave_sum = [](int v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+  };
+  for (int i = threadIdx.x; i <= g.L; i += 64 * NW) offs[i] = g.tab_offs[i];
+  if (threadIdx.x < kOrder / 32) listed[threadIdx.x] = 0;
+  int row[M], id[M];  // this thread's positions of the table
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int pos = t0 + i * 64 * NW + threadIdx.x;
+    row[i] = pos < live ? g.tab_perm[pos] : -1;
+    if ((uint32_t)row[i] >= (uint32_t)g.rows) row[i] = -1;
+    id[i] = row[i] < 0 ? -1 : g.ids[row[i]];
+  }
+  int before = 0, mine = 0, behind = 0;  // (of this wave's share)
+  // (a run of eight loads at a time, on one side of this workgroup's tokens)
   static_assert(kOrder % (8 * 64) == 0, "whole runs");
-  for (int t = threadIdx.x / 64 * 512 + lane; t < t0; t += 512 * NW) {
-    int e[8];
+  for (int r = wave * 512; r < g.rows; r += 512 * NW) {
+    if (r / kOrder == b) continue;
+    int e[8], n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = g.ids[t + 64 * i];
+    for (int i = 0; i < 8; ++i) e[i] = r + 64 * i + lane < g.rows ? g.ids[r + 64 * i + lane] : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) before += (uint32_t)e[i] >= (uint32_t)g.L;
+    for (int i = 0; i < 8; ++i) n += bare(e[i]);
+    if (r < t0) before += n;
+    else behind += n;
   }
   uint64_t m[M];
 #pragma unroll
   for (int i = 0; i < M; ++i) {
-    m[i] = __ballot(bare(t0 + (wave * M + i) * 64 + lane));
+    const int t = t0 + (wave * M + i) * 64 + lane;
+    m[i] = __ballot(t < g.rows && bare(g.ids[t]));
     mine += __builtin_popcountll(m[i]);
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) before += __shfl_xor(before, d, 64);
+  before = wave_sum(before);
+  behind = wave_sum(behind);
   if (lane == 0) {
     count[wave] = before;
     count[16 + wave] = mine;
-  }
-  for (int i = t0 + threadIdx.x; i < min(t0 + kOrder, live); i += 64 * NW) {
-    const int row = g.tab_perm[i];
-    g.order[i] = make_int2(row, (uint32_t)row < (uint32_t)g.rows ? g.ids[row] : -1);
+    count[32 + wave] = behind;
   }
   __syncthreads();
-  int at = live;
-  for (int w = 0; w < NW; ++w) at += count[w] + (w < wave ? count[16 + w] : 0);
+  int ahead = 0, all = 0;  // before this wave's, and in all
+  auto add_up = [&] {
+    ahead = all = 0;
+    for (int w = 0; w < NW; ++w) {
+      ahead += count[w] + (w < wave ? count[16 + w] : 0);
+      all += count[w] + count[16 + w] + count[32 + w];
+    }
+  };
+  add_up();
+  const bool over = live + all > g.rows;
+  if (over) {  // (for the whole grid)
+    int lb = 0, lm = 0, la = 0;
+    for (int i = threadIdx.x; i < live; i += 64 * NW) {
+      const int r = g.tab_perm[i];
+      if ((uint32_t)r >= (uint32_t)g.rows || !bare(g.ids[r])) continue;
+      if (r < t0) ++lb;
+      else if (r >= t0 + kOrder) ++la;
+      else atomicOr(listed + (r - t0) / 32, 1u << (r & 31));
+    }
+    lb = wave_sum(lb);
+    la = wave_sum(la);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const int w = 2 * (wave * M + i);
+      m[i] &= ~((uint64_t)listed[w + 1] << 32 | listed[w]);
+      lm += __builtin_popcountll(m[i]);
+    }
+    if (lane == 0) {
+      count[wave] = before - lb;
+      count[16 + wave] = lm;
+      count[32 + wave] = behind - la;
+    }
+    __syncthreads();
+    add_up();
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int pos = t0 + i * 64 * NW + threadIdx.x;
+    if (pos >= g.rows || (pos >= live && pos < live + all)) continue;
+    int2 o = make_int2(-1, -1);
+    if (bare(id[i])) o.x = over ? row[i] : -1;
+    else if (offs[id[i]] <= pos && pos < offs[id[i] + 1]) o = make_int2(row[i], id[i]);
+    g.order[pos] = o;
+  }
+  int at = live + ahead;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     const int to = at + __builtin_popcountll(m[i] & (((uint64_t)1 << lane) - 1));
-    if (m[i] >> lane & 1 && to < g.rows) g.order[to] = make_int2(t0 + (wave * M + i) * 64 + lane, -1);
+    if (m[i] >> lane & 1 && (uint32_t)to < (uint32_t)g.rows) g.order[to] = make_int2(t0 + (wave * M + i) * 64 + lane, -1);
     at += __builtin_popcountll(m[i]);
   }
 }
@@ -193,10 +266,11 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   static_assert(ASYNC * (STAGES - 1) < 64, "vmcnt range");
   // (The rows lie behind the ring, in one object with it: beside another object the
   // compiler waits for every load into the ring before it reads it.)
-  __shared__ __align__(16) unsigned char ring[STAGES * STAGE + (BM < 32 ? 32 : BM) * 4];
+  static_assert(STAGES * STAGE >= kOrderInts * 4, "the order's counts and ranges");
+  __shared__ __align__(16) unsigned char ring[STAGES * STAGE + BM * 4];
   int *rows = reinterpret_cast<int *>(ring + STAGES * STAGE);
   if ((int)blockIdx.x >= wgs) {
-    order_tokens<NW>(g, blockIdx.x - wgs, rows);
+    order_tokens<NW>(g, blockIdx.x - wgs, reinterpret_cast<int *>(ring));
     return;
   }
   Q8Args tab{};
