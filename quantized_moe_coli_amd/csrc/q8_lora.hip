@@ -78,7 +78,7 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *ld
   int *count = lds;
   uint32_t *listed = reinterpret_cast<uint32_t *>(lds + 48);  // a bit for each of this workgroup's tokens
   int *offs = lds + 48 + kOrder / 32;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
   auto bare = [&](int e) { return (uint32_t)e >= (uint32_t)g.L; };
   auto wave_sum = [](int v) {
@@ -97,17 +97,32 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *ld
     id[i] = row[i] < 0 ? -1 : g.ids[row[i]];
   }
   int before = 0, mine = 0, behind = 0;  // (of this wave's share)
-  // (a run of eight loads at a time, on one side of this workgroup's tokens)
-  static_assert(kOrder % (8 * 64) == 0, "whole runs");
-  for (int r = wave * 512; r < g.rows; r += 512 * NW) {
-    if (r / kOrder == b) continue;
-    int e[8], n = 0;
+  // (Every workgroup counts all tokens, by runs of kOrder, a wave two at a time as long
+  // as they are whole.  8192 and 131072 tokens x 512 x 512 and x 128 x 128 take 28 and
+  // 81 us in all, a million x 64 x 64 846.)
+  constexpr int RUN = kOrder / 64;
+  auto count_run = [&](int r, const int (&e)[RUN]) __attribute__((always_inline)) {
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = r + 64 * i + lane < g.rows ? g.ids[r + 64 * i + lane] : 0;
+    for (int i = 0; i < RUN; ++i) n += __builtin_popcountll(__ballot(bare(e[i])));
+    before += r < t0 ? n : 0;
+    behind += r > t0 ? n : 0;
+  };
+  int r = wave * kOrder;
+  for (; r + (NW + 1) * kOrder <= g.rows; r += 2 * NW * kOrder) {
+    int e[2][RUN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n += bare(e[i]);
-    if (r < t0) before += n;
-    else behind += n;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) e[h][i] = (g.ids + r + h * NW * kOrder + lane)[64 * i];
+    count_run(r, e[0]);
+    count_run(r + NW * kOrder, e[1]);
+  }
+  for (; r < g.rows; r += NW * kOrder) {
+    int e[RUN];
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) e[i] = r != t0 && r + 64 * i + lane < g.rows ? g.ids[r + 64 * i + lane] : 0;
+    count_run(r, e);
   }
   uint64_t m[M];
 #pragma unroll
@@ -116,8 +131,6 @@ __device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *ld
     m[i] = __ballot(t < g.rows && bare(g.ids[t]));
     mine += __builtin_popcountll(m[i]);
   }
-  before = wave_sum(before);
-  behind = wave_sum(behind);
   if (lane == 0) {
     count[wave] = before;
     count[16 + wave] = mine;
