@@ -379,10 +379,11 @@ coli_status coli_swiglu_quant_token(int32_t dtype, const void *g, int64_t ldg,
  * coli_quant_act_token makes them (so their operand is not y as it was rounded to
  * a 16-bit type).  Each output may be NULL: q and s together, and one of y_out
  * and q must be there.  h_out and y_out may be x or res themselves, with the same
- * row stride, but not one another.  A row whose h holds an infinity gets NaN where
- * it stands in y and 0 elsewhere, one with a NaN gets NaN all along; s = NaN and
- * q = 0 in both.  eps finite and above 0; n at least 1 and at most 131072, with q a
- * multiple of 32 and at most 131040; 0 <= T <= 2^25 (a row may be one head's). */
+ * row stride (of more than one row, another is refused), but not one another.  A row
+ * whose h holds an infinity gets NaN where it stands in y and 0 elsewhere, one with
+ * a NaN gets NaN all along; s = NaN and q = 0 in both.  eps finite and above 0; n at
+ * least 1 and at most 131072, with q a multiple of 32 and at most 131040;
+ * 0 <= T <= 2^25 (a row may be one head's). */
 coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx,
                                      const void *res, int64_t ldres,
                                      const float *gain, float eps, int32_t T,

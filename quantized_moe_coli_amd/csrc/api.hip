@@ -456,6 +456,11 @@ coli_status coli_rmsnorm_quant_token(int32_t dtype, const void *x, int64_t ldx, 
         (h && !rows_ok(dtype, h, ldh, n)) || (y && !rows_ok(dtype, y, ldy, n)) || !aligned(gain, 4) ||
         !aligned(q, 16) || !aligned(s, 4))
       return COLI_ERR_INVALID_ARG;
+    // (an output on an input of another stride would write rows that are still to be read)
+    auto shifted = [&](const void *out, int64_t ld) {
+      return out && T > 1 && ((out == x && ld != ldx) || (out == res && ld != ldres));
+    };
+    if (shifted(h, ldh) || shifted(y, ldy)) return COLI_ERR_INVALID_ARG;
     const coli_status st = check_device();
     if (st != COLI_OK) return st;
     const coli::NormArgs a{x, res, ldx, ldres, gain, eps, T, n, 1.0 / n, h, y, ldh, ldy, q, s};

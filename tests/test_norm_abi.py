@@ -26,3 +26,20 @@ def test_rmsnorm_quant_token():
 def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="device tensor"):
         B.coli_rmsnorm_quant_token(torch.zeros(2, 64), None, 1e-6, y=torch.zeros(2, 64))
+
+
+def test_outputs_on_inputs_of_another_row_stride():
+    """A row written where another row is read: refused, as long as there is another row."""
+    X, R, Y = P, 2 * P, 3 * P
+    good = dict(dt=1, x=X, ldx=64, res=R, ldr=96, gain=P, eps=1e-6, T=2, n=64, h=4 * P, ldh=64, y=Y, ldy=64,
+                q=5 * P, s=P, st=None)
+    refuse("coli_rmsnorm_quant_token", good, [
+        dict(h=X, ldh=96), dict(h=R, ldh=64), dict(y=X, ldy=96), dict(y=R, ldy=64), dict(h=X, ldh=65),
+        dict(y=X, ldy=96, h=None, ldh=0), dict(h=R, ldh=128, y=None, ldy=0), dict(h=R, ldh=96, y=X, ldy=96),
+        dict(res=X, h=X, ldh=64)])
+    fn = B.lib().coli_rmsnorm_quant_token
+    if not torch.cuda.is_available():
+        for change in (dict(h=X), dict(h=R, ldh=96), dict(y=X), dict(y=R, ldy=96), dict(h=R, ldh=96, y=X),
+                       dict(T=1, h=X, ldh=96), dict(T=1, y=R, ldy=64), dict(res=None, ldr=0, h=X),
+                       dict(res=None, ldr=0, h=None, ldh=0, y=X)):
+            assert fn(*dict(good, **change).values()) == B.COLI_ERR_DEVICE, change
