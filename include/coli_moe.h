@@ -433,21 +433,22 @@ size_t coli_lora_workspace_bytes(int32_t max_tokens, int32_t rank);
  * coli_gemm_q8's, bit for bit.  x [T][K], row stride ldx, are the activations of
  * which q and s are the codes, in dtype like a, b and y.  ids [T] int32; offs
  * [L + 1] and perm [T] are coli_moe_dispatch's tables of ids as one slot a token
- * (k = 1, E = L), which one call makes for all projections of a batch.  They list no
- * token twice.  A token whose id is in [0, L) and that they list under another
- * adapter, or not at all, gets an undefined row, and no other token's row changes for
- * it; whether a token without an adapter is listed does not matter.
+ * (k = 1, E = L), which one call makes for all projections of a batch.  They list
+ * no token twice.  A token whose id is in [0, L) and that they list under another
+ * adapter, or not at all, gets an undefined row, and no other token's row changes
+ * for it; whether a token without an adapter is listed does not matter.
  * u is an fp32 sum, not rounded to a 16-bit type: it enters the second product to
- * 2^-17 of its value where dtype is one, and to 2^-24 in fp32.  The adapters'
- * part is summed by itself in fp32, whole or by 32 ranks or more, and joins the
- * projection's part and the bias by fp32 additions, five at most, each rounded at
- * the size of its result; that is rounded to dtype.  The order of the fp32 sums
- * goes by the batch's sizes, so a row with an adapter may differ in the last bits
- * of fp32 from batch to batch; the same call gives the same bits.  An adapter that
- * holds a NaN or an infinity makes only its own tokens' results NaN or infinite.
- * The rest, and the limits, as for coli_gemm_q8; T * K of 2^32 or more may return
- * COLI_ERR_UNSUPPORTED.
- * COLI_ERR_WORKSPACE for a missing, misaligned or short workspace. */
+ * 2^-17 of its value where dtype is one, and to 2^-24 in fp32 (u and scale_l * u
+ * past 3.39e38 may give NaN).  The adapters' part is summed by itself in fp32,
+ * whole or by 32 or 64 ranks at a time, and joins the projection's part and the
+ * bias by fp32 additions, five at most, each rounded at the size of its result;
+ * that is rounded to dtype.  The order of the fp32 sums goes by the batch's sizes,
+ * so a row with an adapter may differ in the last bits of fp32 from batch to
+ * batch; the same call gives the same bits.  An adapter that holds a NaN or an
+ * infinity makes only its own tokens' results NaN or infinite.  The rest, and the
+ * limits, as for coli_gemm_q8; T * K of 2^32 or more may return
+ * COLI_ERR_UNSUPPORTED.  COLI_ERR_WORKSPACE for a missing, misaligned or short
+ * workspace. */
 coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T,
                               const uint8_t *w, const float *ws, int32_t N,
                               int32_t K, const float *bias,

@@ -115,8 +115,9 @@ __device__ __forceinline__ void b_operand(const unsigned char *row, F place, int
 // together, as whole lines into LDS of its own, D of them on the way, without a
 // barrier.  (300 tokens x 4000 channels x 6144 with 64 adapters of rank 16, 64 and
 // 128: 40, 51 and 72 us for both launches, with each lane reading its own token's
-// rows into registers 45, 97 and 159.  Asking for the rows' lines while the sums are
-// still made does not help: 28, 37 and 55 us instead of 28, 33 and 46 at 61 x 6144.)
+// rows into registers 45, 97 and 159; the product's alone 28, 37 and 48.  Asking for
+// the rows' lines while the sums are still made does not help: 28, 37 and 55 us
+// instead of 28, 33 and 46 at 61 x 6144.)
 // u's parts are added, cut into bfloat16 pieces and put in LDS for all the waves
 // before.  Ranks go by chunks of 128 bytes of b's rows.  Lane (li, lg) has channels 4
 // lg .. of token li, and takes its own adapter's results and no other's, whatever
@@ -301,11 +302,11 @@ struct LoraRing {
 // instruction, 3 R / 8 of them in binary32: parts of an adapter that lie below half a
 // step of a large result were lost one by one.)
 //
-// 8192 x 6144 x 6144, launches of the product alone: 290 us where no token has an
-// adapter, 295 with one of rank 16, 306 with eight of rank 64, 323 with sixteen of
-// rank 128 (least of 12).  Each adapter of a group costs a wait for its rows, so
-// where a group has many they are what it waits for: 509 x 6144 x 6144 of rank 16 37
-// us with one, 45 with 64 in any order.
+// 8192 x 6144 x 6144, the product's launch alone: 288 us where no token has an
+// adapter, 292 with one of rank 16, 301 with eight of rank 64, 322 with sixteen of
+// rank 128 (least of 24).  Each adapter of a group costs a wait for its rows, so
+// where a group has many they are what it waits for: 509 x 6144 x 6144 of rank 16 38
+// us with one, 45 with 64 in any order, of rank 64 56.
 template <int DT, int BM, int BN, int WM, int WN>
 struct LoraTile {
   typedef typename Elem<DT>::type T;

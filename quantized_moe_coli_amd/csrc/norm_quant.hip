@@ -12,11 +12,14 @@
 // scale is NaN and its codes 0, as the other quantisers have it.
 //
 // Bound by the memory: every element of x, res, h, y and q is moved once, as
-// long as a row fits the registers of the threads that share it; longer rows
-// (past 32768 elements) are read three times.  8192 x 6144 bfloat16 with h, y and
+// long as a row fits the registers of the threads that share it.  What lies past a
+// row's first 32768 elements, or 8192 where rows are loaded by elements, is read
+// three times with codes, twice without.  8192 x 6144 bfloat16 with h, y and
 // codes 95.5 us (453 MB, 4.7 TB/s; a copy reaches 5.06), float32 with h and y 148 us
-// (5.4 TB/s); one row 4.4 us, of which a launch is 2, two sums over its workgroup
-// the most of the rest.
+// (5.4 TB/s); 2048 x 16384 69 us (4.4 TB/s), 256 x 65536 38 us (3.9); rows of a wider
+// buffer that start at any element 1.4 to 1.7 times as long (638 x 9952 35 us, 20 where
+// aligned, 2048 x 16384 103).  One row of 6144 4.4 us, of which a launch is 2, two sums
+// over its workgroup the most of the rest; of 131040 43 us, by one workgroup.
 #include <algorithm>
 #include <type_traits>
 
@@ -283,7 +286,9 @@ hipError_t launch_norm_quant(int dt, const NormArgs &a, hipStream_t st) {
     // Few rows: a thread for every piece, the shortest way through a row; many: four
     // pieces a thread, more rows at a time.  With h, y and codes in bfloat16 (us, the one
     // / the other):
-    //   192 columns, 33564 rows, by 16 and by 64 threads 14.9 / 26.5; 512 x 4096 8.2 / 5.7
+    //   by 16 and by 64 threads, 2304, 8192 and 33564 rows:
+    //     192 columns  4.5 / 4.2, 5.9 / 8.3, 14.9 / 25.1;   320  5.8 / 4.3, 9.0 / 9.3, 22.2 / 25.8
+    //     384          5.9 / 4.4, 9.3 / 9.5, 23.9 / 26.3;   512  7.2 / 4.5, 11.6 / 10.1, 34.5 / 34.9
     //   512 columns:   256 rows 3.1 / 3.4, 1024 3.4 / 3.7, 4096 7.3 / 7.1
     //   2048 columns:  256 rows 3.6 / 6.8, 1024 7.5 / 9.3, 4096 16.6 / 16.5
     //   6144 columns:  16 rows 4.6 / 5.6, 256 6.2 / 7.3, 512 10.6 / 9.5, 4096 63.6 / 46.4

@@ -94,7 +94,9 @@ struct Q8LoraArgs : Q8Args {
   const float *scale;  // [L] or null
   const int32_t *ids, *tab_offs, *tab_perm;
   float *u;
-  int2 *order;  // [rows] tokens and their adapters, by adapter, those without one last; null: as they are
+  // [rows] tokens and their adapters, by adapter, those without one (-1) last, token -1: none;
+  // null: as they are
+  int2 *order;
   int L, R, slices;
   bool pieces;  // u as bfloat16 pieces, times the adapters' scales, by position in order (lora.hpp)
 };

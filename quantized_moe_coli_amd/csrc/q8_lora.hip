@@ -391,8 +391,10 @@ int slices_of(int T, int tiles, int most) {
 
 bool tiled(Variant v) { return v == kTile128 || v == kTile128Deep || v == kTile256; }
 
-// As without adapters, but for the sweep, which has no form with them: the
-// 128 x 128 tiles are within 13 % of the best of the forms there.
+// As without adapters, by times of the product alone: with them the forms have not been
+// compared (the 64 x 64 ring has 128 registers then, and in fp32 keeps ten values in
+// memory).  The sweep has no form with adapters: the 128 x 128 tiles are within 13 % of
+// the best of the forms there.
 Variant lora_variant(const Q8LoraArgs &a) {
   const Variant v = dense_variant(a);
   return v == kSweep64 ? kTile128 : v;
@@ -425,6 +427,8 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
   const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : a.R <= 64 ? 4 : 8;
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                    (uint64_t)a.ldx * (dt == COLI_F32 ? 4 : 2) % 16 == 0;
+  // (x that starts at any element goes by 16 tokens: both launches of 300 tokens x 4000
+  // x 6144 of rank 16 and 128 take 38.5 and 57 us, with aligned rows 36 and 49.)
   // Tokens of a tile: a tile costs its tokens' and its adapter's rows, and a CU
   // works through its tiles one after another.  (8192 x 6144 of rank 64, 16 adapters:
   // 272 tiles of 32 tokens 52-56 us, 187 of 48 38-43.)
