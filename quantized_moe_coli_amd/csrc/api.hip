@@ -498,7 +498,7 @@ coli_status coli_gemm_q8_lora(const int8_t *q, const float *s, int32_t T, const 
                               void *stream) {
   return guarded([&] {
     if (!dtype_ok(dtype) || T < 0 || T > kMaxTokens || N < 1 || K <= 0 || K % 32 || K > kMaxQ8Cols || !lora ||
-        lora->n_adapters < 1 || lora->n_adapters > 1024 || !lora_rank_ok(lora->rank))
+        lora->n_adapters < 1 || lora->n_adapters > coli::kMaxAdapters || !lora_rank_ok(lora->rank))
       return COLI_ERR_INVALID_ARG;
     if (T == 0) return COLI_OK;
     if (!q || !s || !w || !ws || !rows_ok(dtype, y, ldy, N) || !rows_ok(dtype, x, ldx, K) || !lora->a ||

@@ -87,6 +87,7 @@ hipError_t launch_gemm_q8(int dt, const Q8Args &a, hipStream_t st);
 // y's type; ids [rows] a token's adapter (none outside [0, L)), tab_offs [L + 1]
 // and tab_perm [rows] the tokens by adapter; u [slices][rows][R] the tokens'
 // products with a, in parts of K.
+constexpr int kMaxAdapters = 1024;  // (their ranges lie in LDS)
 struct Q8LoraArgs : Q8Args {
   const void *x;  // [rows][ldx]
   int64_t ldx;

@@ -67,7 +67,6 @@ __device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int 
 // Workgroup b writes the table's part of positions kOrder b .. and the tokens without
 // an adapter among tokens kOrder b ..; those before and behind them it counts itself.
 constexpr int kOrder = 1024;
-constexpr int kMaxAdapters = 1024;
 constexpr int kOrderInts = 48 + kOrder / 32 + kMaxAdapters + 1;  // of LDS
 
 template <int NW>
