@@ -64,129 +64,152 @@ __device__ __forceinline__ void put_u(const Q8LoraArgs &g, int sl, int row, int 
 // none.  Where listed tokens and those without an adapter are more than there are,
 // some of these are listed: they keep the table's place and are passed over behind it.
 //
-// Workgroup b writes the table's part of positions kOrder b .. and the tokens without
-// an adapter among tokens kOrder b ..; those before and behind them it counts itself.
+// Workgroup b has `per` blocks of kOrder tokens and positions.  It writes the table's
+// part of its positions and its tokens without an adapter; the others it counts itself.
+// (Past 256 blocks, one for each CU, a workgroup takes several, since each reads all
+// ids: a million tokens x 64 x 64 574 us in all, with a block each 846;
+// 8192 x 512 x 512 28, 131072 x 128 x 128 82.)
 constexpr int kOrder = 1024;
+constexpr int kOrderWgs = 256;
 constexpr int kOrderInts = 48 + kOrder / 32 + kMaxAdapters + 1;  // of LDS
 
 template <int NW>
-__device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int *lds) {
+__device__ __forceinline__ void order_tokens(const Q8LoraArgs &g, int b, int per, int *lds) {
   static_assert(NW <= 16 && kOrder % (64 * NW) == 0 && kOrder <= 32 * 64 * NW, "whole rounds");
-  constexpr int M = kOrder / 64 / NW;
-  // for each wave: tokens without an adapter before this workgroup's, its own, and behind
+  constexpr int M = kOrder / 64 / NW, RUN = kOrder / 64;
+  // for each wave: tokens without an adapter before this workgroup's, from its first on, in a block
   int *count = lds;
-  uint32_t *listed = reinterpret_cast<uint32_t *>(lds + 48);  // a bit for each of this workgroup's tokens
+  uint32_t *listed = reinterpret_cast<uint32_t *>(lds + 48);  // a bit for each token of a block
   int *offs = lds + 48 + kOrder / 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = b * kOrder, live = min(max(g.tab_offs[g.L], 0), g.rows);
+  const int first = b * per * kOrder, end = min(first + per * kOrder, g.rows);
+  if (first >= end) return;
+  const int live = min(max(g.tab_offs[g.L], 0), g.rows);
   auto bare = [&](int e) { return (uint32_t)e >= (uint32_t)g.L; };
   auto wave_sum = [](int v) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
     return v;
   };
+  auto waves_sum = [&](const int *c, int n) {
+    int v = 0;
+    for (int w = 0; w < n; ++w) v += c[w];
+    return v;
+  };
   for (int i = threadIdx.x; i <= g.L; i += 64 * NW) offs[i] = g.tab_offs[i];
-  if (threadIdx.x < kOrder / 32) listed[threadIdx.x] = 0;
-  int row[M], id[M];  // this thread's positions of the table
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const int pos = t0 + i * 64 * NW + threadIdx.x;
-    row[i] = pos < live ? g.tab_perm[pos] : -1;
-    if ((uint32_t)row[i] >= (uint32_t)g.rows) row[i] = -1;
-    id[i] = row[i] < 0 ? -1 : g.ids[row[i]];
-  }
-  int before = 0, mine = 0, behind = 0;  // (of this wave's share)
-  // (Every workgroup counts all tokens, by runs of kOrder, a wave two at a time as long
-  // as they are whole.  8192 and 131072 tokens x 512 x 512 and x 128 x 128 take 28 and
-  // 81 us in all, a million x 64 x 64 846.)
-  constexpr int RUN = kOrder / 64;
-  auto count_run = [&](int r, const int (&e)[RUN]) __attribute__((always_inline)) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) n += __builtin_popcountll(__ballot(bare(e[i])));
-    before += r < t0 ? n : 0;
-    behind += r > t0 ? n : 0;
-  };
-  int r = wave * kOrder;
-  for (; r + (NW + 1) * kOrder <= g.rows; r += 2 * NW * kOrder) {
-    int e[2][RUN];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < RUN; ++i) e[h][i] = (g.ids + r + h * NW * kOrder + lane)[64 * i];
-    count_run(r, e[0]);
-    count_run(r + NW * kOrder, e[1]);
-  }
-  for (; r < g.rows; r += NW * kOrder) {
-    int e[RUN];
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) e[i] = r != t0 && r + 64 * i + lane < g.rows ? g.ids[r + 64 * i + lane] : 0;
-    count_run(r, e);
-  }
-  uint64_t m[M];
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const int t = t0 + (wave * M + i) * 64 + lane;
-    m[i] = __ballot(t < g.rows && bare(g.ids[t]));
-    mine += __builtin_popcountll(m[i]);
-  }
-  if (lane == 0) {
-    count[wave] = before;
-    count[16 + wave] = mine;
-    count[32 + wave] = behind;
-  }
-  __syncthreads();
-  int ahead = 0, all = 0;  // before this wave's, and in all
-  auto add_up = [&] {
-    ahead = all = 0;
-    for (int w = 0; w < NW; ++w) {
-      ahead += count[w] + (w < wave ? count[16 + w] : 0);
-      all += count[w] + count[16 + w] + count[32 + w];
-    }
-  };
-  add_up();
-  const bool over = live + all > g.rows;
-  if (over) {  // (for the whole grid)
-    int lb = 0, lm = 0, la = 0;
-    for (int i = threadIdx.x; i < live; i += 64 * NW) {
-      const int r = g.tab_perm[i];
-      if ((uint32_t)r >= (uint32_t)g.rows || !bare(g.ids[r])) continue;
-      if (r < t0) ++lb;
-      else if (r >= t0 + kOrder) ++la;
-      else atomicOr(listed + (r - t0) / 32, 1u << (r & 31));
-    }
-    lb = wave_sum(lb);
-    la = wave_sum(la);
-    __syncthreads();
+  int row[M], id[M];  // this thread's positions of the table in a block
+  auto load_table = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      const int w = 2 * (wave * M + i);
-      m[i] &= ~((uint64_t)listed[w + 1] << 32 | listed[w]);
-      lm += __builtin_popcountll(m[i]);
+      const int pos = t0 + i * 64 * NW + threadIdx.x;
+      row[i] = pos < live ? g.tab_perm[pos] : -1;
+      if ((uint32_t)row[i] >= (uint32_t)g.rows) row[i] = -1;
+      id[i] = row[i] < 0 ? -1 : g.ids[row[i]];
+    }
+  };
+  load_table(first);
+  {
+    // by blocks, a wave two at a time as long as they are whole
+    int before = 0, rest = 0;
+    auto count_run = [&](int r, const int (&e)[RUN]) __attribute__((always_inline)) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) n += __builtin_popcountll(__ballot(bare(e[i])));
+      before += r < first ? n : 0;
+      rest += r < first ? 0 : n;
+    };
+    int r = wave * kOrder;
+    for (; r + (NW + 1) * kOrder <= g.rows; r += 2 * NW * kOrder) {
+      int e[2][RUN];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) e[h][i] = (g.ids + r + h * NW * kOrder + lane)[64 * i];
+      count_run(r, e[0]);
+      count_run(r + NW * kOrder, e[1]);
+    }
+    for (; r < g.rows; r += NW * kOrder) {
+      int e[RUN];
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) e[i] = r + 64 * i + lane < g.rows ? g.ids[r + 64 * i + lane] : 0;
+      count_run(r, e);
     }
     if (lane == 0) {
-      count[wave] = before - lb;
-      count[16 + wave] = lm;
-      count[32 + wave] = behind - la;
+      count[wave] = before;
+      count[16 + wave] = rest;
     }
+  }
+  int before = 0, all = 0;  // tokens without an adapter before the block and in all, as they lie behind the table's
+  bool over = false;
+  for (int t0 = first; t0 < end; t0 += kOrder) {
+    if (threadIdx.x < kOrder / 32) listed[threadIdx.x] = 0;
+    uint64_t m[M];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const int t = t0 + (wave * M + i) * 64 + lane;
+      m[i] = __ballot(t < g.rows && bare(g.ids[t]));
+      mine += __builtin_popcountll(m[i]);
+    }
+    if (lane == 0) count[32 + wave] = mine;
     __syncthreads();
-    add_up();
-  }
+    if (t0 == first) {
+      before = waves_sum(count, NW);
+      all = before + waves_sum(count + 16, NW);
+      over = live + all > g.rows;  // (in every workgroup)
+    }
+    if (over) {
+      int lb = 0, la = 0;  // listed tokens without an adapter before this workgroup's, and in all
+      for (int i = threadIdx.x; i < live; i += 64 * NW) {
+        const int r = g.tab_perm[i];
+        if ((uint32_t)r >= (uint32_t)g.rows || !bare(g.ids[r])) continue;
+        ++la;
+        if (r < first) ++lb;
+        if (r >= t0 && r < t0 + kOrder) atomicOr(listed + (r - t0) / 32, 1u << (r & 31));
+      }
+      lb = wave_sum(lb);
+      la = wave_sum(la);
+      __syncthreads();
+      mine = 0;
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const int pos = t0 + i * 64 * NW + threadIdx.x;
-    if (pos >= g.rows || (pos >= live && pos < live + all)) continue;
-    int2 o = make_int2(-1, -1);
-    if (bare(id[i])) o.x = over ? row[i] : -1;
-    else if (offs[id[i]] <= pos && pos < offs[id[i] + 1]) o = make_int2(row[i], id[i]);
-    g.order[pos] = o;
-  }
-  int at = live + ahead;
+      for (int i = 0; i < M; ++i) {
+        const int w = 2 * (wave * M + i);
+        m[i] &= ~((uint64_t)listed[w + 1] << 32 | listed[w]);
+        mine += __builtin_popcountll(m[i]);
+      }
+      if (lane == 0) {
+        count[wave] = lb;
+        count[16 + wave] = la;
+        count[32 + wave] = mine;
+      }
+      __syncthreads();
+      if (t0 == first) {
+        before -= waves_sum(count, NW);
+        all -= waves_sum(count + 16, NW);
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-    const int to = at + __builtin_popcountll(m[i] & (((uint64_t)1 << lane) - 1));
-    if (m[i] >> lane & 1 && (uint32_t)to < (uint32_t)g.rows) g.order[to] = make_int2(t0 + (wave * M + i) * 64 + lane, -1);
-    at += __builtin_popcountll(m[i]);
+    for (int i = 0; i < M; ++i) {
+      const int pos = t0 + i * 64 * NW + threadIdx.x;
+      if (pos >= g.rows || (pos >= live && pos < live + all)) continue;
+      int2 o = make_int2(-1, -1);
+      if (bare(id[i])) o.x = over ? row[i] : -1;
+      else if (offs[id[i]] <= pos && pos < offs[id[i] + 1]) o = make_int2(row[i], id[i]);
+      g.order[pos] = o;
+    }
+    int at = live + before + waves_sum(count + 32, wave);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const int to = at + __builtin_popcountll(m[i] & (((uint64_t)1 << lane) - 1));
+      if (m[i] >> lane & 1 && (uint32_t)to < (uint32_t)g.rows)
+        g.order[to] = make_int2(t0 + (wave * M + i) * 64 + lane, -1);
+      at += __builtin_popcountll(m[i]);
+    }
+    if (t0 + kOrder < end) {
+      before += waves_sum(count + 32, NW);
+      load_table(t0 + kOrder);
+      __syncthreads();  // the counts and bits have been read
+    }
   }
 }
 
@@ -282,7 +305,8 @@ __global__ __launch_bounds__(256) void k_lora_down(Q8LoraArgs g, int wgs) {
   __shared__ __align__(16) unsigned char ring[STAGES * STAGE + BM * 4];
   int *rows = reinterpret_cast<int *>(ring + STAGES * STAGE);
   if ((int)blockIdx.x >= wgs) {
-    order_tokens<NW>(g, blockIdx.x - wgs, reinterpret_cast<int *>(ring));
+    const int blocks = (g.rows + kOrder - 1) / kOrder;
+    order_tokens<NW>(g, blockIdx.x - wgs, (blocks + kOrderWgs - 1) / kOrderWgs, reinterpret_cast<int *>(ring));
     return;
   }
   Q8Args tab{};
@@ -442,7 +466,7 @@ hipError_t launch_gemm_q8_lora(int dt, Q8LoraArgs a, void *workspace, hipStream_
   const int tiles = one ? a.rows : a.rows / bm + std::min(a.rows, a.L);  // at most
   a.slices = a.pieces ? 1 : slices_of(a.rows, one ? a.rows : (a.rows + bm - 1) / bm, lora_parts(kShapes[v].bm));
   const int wgs = (int)(((int64_t)tiles * a.slices + 7) / 8 * 8);
-  const int extra = (a.rows + kOrder - 1) / kOrder;
+  const int extra = std::min((a.rows + kOrder - 1) / kOrder, kOrderWgs);  // workgroups of the order
   if (one) a.order = nullptr;
   return by_dtype(dt, [&](auto dtc) {
     constexpr int DT = decltype(dtc)::value;

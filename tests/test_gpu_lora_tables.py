@@ -11,8 +11,9 @@ from test_gpu_lora import Case, some_ids, tables
 from test_gpu_q8 import gen
 
 pytestmark = pytest.mark.gpu
-# up to 64 tokens without an order, rings by it, tiles of 128 and 256, several workgroups of the order
-SIZES = [(40, 1024), (65, 333), (64, 66000), (300, 4000), (600, 6145), (1500, 6144), (2500, 517), (9001, 130)]
+# up to 64 tokens without an order, rings by it, tiles of 128 and 256, several workgroups of the
+# order, and of several blocks each
+SIZES = [(40, 1024), (65, 333), (64, 66000), (300, 4000), (600, 6145), (1500, 6144), (2500, 517), (9001, 130), (307277, 20)]
 
 
 def changed(ids, L, what, seed):
